@@ -1,0 +1,407 @@
+"""Cases and plain forms of the operators around an 8-bit mixture-of-experts block:
+
+  router    expert choice by softmax or sigmoid scores with a selection bias, expert groups,
+            top-k and renormalised weights, alone or together with the grouping of the pairs
+  norm      residual addition, root-mean-square norm and 8-bit rows with scales
+  quantize  bf16 rows to int8 with one scale per row, scattered into grouped rows
+  gemm      grouped int8 x int8 product with a scale per row and per output channel
+
+`run` computes a case in elementary torch operations, or, with `own` set, through the
+library's entry points on the same state.  `exact` gives the results in 64 bits.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+TINY = 2.0 ** -100   # rows or blocks whose largest magnitude is below this count as zero
+
+
+def listed():
+    return [
+        # one decoding step of 64 sequences: router logits to weights and expert groups
+        dict(name="router decode grouped", op="router", T=64, E=256, k=8, dtype="f32",
+             scoring="sigmoid", bias=True, n_group=8, topk_group=4, group_top=2, renorm=True,
+             scale=2.5, route=True),
+        # a prefill chunk through the same router
+        dict(name="router prefill", op="router", T=8192, E=256, k=8, dtype="f32",
+             scoring="sigmoid", bias=True, n_group=8, topk_group=4, group_top=2, renorm=True,
+             scale=2.5, route=False),
+        # softmax router of a model without groups, logits straight from a bf16 product
+        dict(name="router softmax bf16", op="router", T=4099, E=128, k=8, dtype="bf16",
+             scoring="softmax", bias=False, n_group=1, topk_group=1, group_top=1, renorm=False,
+             scale=1.0, route=True),
+        # pre-norm of a decoding step, FP8 rows for a block-scaled product
+        dict(name="norm decode fp8", op="norm", T=64, H=7168, fmt="fp8", major="K", residual=True,
+             wdtype="bf16", y=True),
+        # the same for a prefill chunk, scales laid out for 128-row tiles
+        dict(name="norm prefill fp8", op="norm", T=8192, H=7168, fmt="fp8", major="MN",
+             residual=True, wdtype="bf16", y=True),
+        # int8 rows for the int8 product, odd number of tokens
+        dict(name="norm int8", op="norm", T=4099, H=2048, fmt="int8", major="K", residual=True,
+             wdtype="f32", y=True),
+        # grouped int8 rows of a middle-sized expert layer (top-8)
+        dict(name="quantize scatter", op="quantize", T=512, K=2048, k=8),
+        # the intermediate of a prefill chunk, one row per (token, slot) pair
+        dict(name="quantize rows", op="quantize", T=65536, K=2048, k=1),
+        # a dense projection of one token
+        dict(name="gemm one token", op="gemm", R=1, N=4096, K=7168, E=1, gated=False, out="bf16",
+             skew=False),
+        # gate and up products of 128 experts, about 32 rows each
+        dict(name="gemm experts gated", op="gemm", R=4096, N=1536, K=2048, E=128, gated=True,
+             out="bf16", skew=False),
+        # gate and up products of a prefill chunk, skewed routing with empty experts
+        dict(name="gemm prefill gated", op="gemm", R=16384, N=4096, K=7168, E=32, gated=True,
+             out="bf16", skew=True),
+        # a dense down projection of a prefill chunk
+        dict(name="gemm prefill dense", op="gemm", R=8191, N=7168, K=2048, E=1, gated=False,
+             out="f32", skew=False),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["router", "norm", "quantize", "gemm", "gemm"])
+    if op == "router":
+        n_group = rng.choice([1, 1, 2, 4, 8])
+        gs = rng.randint(2, max(2, 512 // n_group)) if n_group > 1 else rng.randint(8, 512)
+        topk_group = rng.randint(1, n_group)
+        k = rng.randint(1, min(16, topk_group * gs))
+        return dict(op=op, T=_log(rng, 1, 8192), E=n_group * gs, k=k,
+                    dtype=rng.choice(["f32", "bf16"]), scoring=rng.choice(["softmax", "sigmoid"]),
+                    bias=rng.random() < 0.6, n_group=n_group, topk_group=topk_group,
+                    group_top=rng.choice([1, 2]), renorm=rng.random() < 0.7,
+                    scale=rng.choice([1.0, 2.5]), route=rng.random() < 0.5)
+    if op == "norm":
+        fmt = rng.choice(["none", "fp8", "mxfp8", "int8"])
+        step = 128 if fmt in ("fp8", "mxfp8") else 16
+        H = step * _log(rng, 1, 7168 // step)
+        return dict(op=op, T=_log(rng, 1, 8192), H=H, fmt=fmt, major=rng.choice(["K", "MN"]),
+                    residual=rng.random() < 0.7, wdtype=rng.choice(["f32", "bf16"]),
+                    y=fmt == "none" or rng.random() < 0.5)
+    if op == "quantize":
+        k = rng.choice([1, 1, 2, 4, 8])
+        T = _log(rng, 1, 65536 // k)
+        return dict(op=op, T=T, K=16 * _log(rng, 4, 2048 // 16), k=k)
+    E = rng.choice([1, 1, _log(rng, 2, 128)])
+    gated = rng.random() < 0.5
+    R, N, K = _log(rng, 1, 16384), 2 * _log(rng, 32, 4096), 16 * _log(rng, 4, 448)
+    while R * N * K > 4096 * 7168 * 16384 or E * N * K > 32 * 4096 * 7168:
+        R, N = max(1, R // 2), max(64, N // 2)
+        K = max(64, K // 32 * 16)
+    return dict(op="gemm", R=R, N=N, K=K, E=E, gated=gated, out=rng.choice(["bf16", "f32"]),
+                skew=E > 1 and rng.random() < 0.5)
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(int(seed))
+
+
+def _empty(*shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="cuda")
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    s = dict(case)
+    if case["op"] == "router":
+        T, E, k = case["T"], case["E"], case["k"]
+        # router logits: a spread per token and experts that are favoured throughout
+        logits = randn(T, E) * 1.5 + randn(1, E)
+        s["logits"] = logits.to(torch.bfloat16) if case["dtype"] == "bf16" else logits
+        s["bias"] = randn(E) * 0.1 if case["bias"] else None
+        s["ids"], s["w"] = _empty(T, k, dtype=torch.int32), _empty(T, k, dtype=torch.float32)
+        s["m_indptr"] = _empty(E + 1, dtype=torch.int32)
+        s["perm"], s["inv_perm"] = _empty(T * k, dtype=torch.int32), _empty(T * k, dtype=torch.int32)
+        # chunks of 1024 pairs, a count per expert each, and the status words
+        s["ws"] = _empty(4096 + 8 * E * (T * k // 1024 + 2), dtype=torch.uint8)
+    elif case["op"] == "norm":
+        T, H = case["T"], case["H"]
+        cols = 1.0 + 20.0 * (torch.rand(H, generator=g, device="cuda") < 0.002)  # outlier channels
+        s["x"] = (randn(T, H) * cols).to(torch.bfloat16)
+        s["residual"] = (randn(T, H) * cols * 2.0).to(torch.bfloat16) if case["residual"] else None
+        w = 1.0 + 0.1 * randn(H)
+        s["weight"] = w.to(torch.bfloat16) if case["wdtype"] == "bf16" else w
+        s["eps"] = 1e-6
+        s["h"] = _empty(T, H, dtype=torch.bfloat16) if case["residual"] else None
+        s["y"] = _empty(T, H, dtype=torch.bfloat16) if case["y"] else None
+        fmt, mn = case["fmt"], case["major"] == "MN"
+        s["q"] = s["q_scale"] = None
+        if fmt == "fp8":
+            s["q"] = _empty(T, H, dtype=torch.float8_e4m3fn)
+            s["q_scale"] = _empty(*((H // 128, T) if mn else (T, H // 128)), dtype=torch.float32)
+        elif fmt == "mxfp8":
+            s["q"] = _empty(T, H, dtype=torch.float8_e4m3fn)
+            s["q_scale"] = _empty(*((H // 128, T, 4) if mn else (T, H // 32)), dtype=torch.uint8)
+        elif fmt == "int8":
+            s["q"], s["q_scale"] = _empty(T, H, dtype=torch.int8), _empty(T, dtype=torch.float32)
+    elif case["op"] == "quantize":
+        T, K, k = case["T"], case["K"], case["k"]
+        s["x"] = (randn(T, K) * torch.exp(0.7 * randn(T, 1))).to(torch.bfloat16)
+        # destination rows: the pairs in some grouped order
+        s["inv_perm"] = (torch.randperm(T * k, generator=g, device="cuda").to(torch.int32)
+                         if k > 1 else None)
+        s["q"], s["q_scale"] = _empty(T * k, K, dtype=torch.int8), _empty(T * k, dtype=torch.float32)
+    else:
+        R, N, K, E = case["R"], case["N"], case["K"], case["E"]
+        code = lambda *sh: (torch.randn(*sh, generator=g, device="cuda", dtype=torch.float16)  # noqa: E731
+                            * 36).round_().clamp_(-127, 127).to(torch.int8)
+        s["a"], s["b"] = code(R, K), code(E, N, K)
+        s["a_scale"] = 0.03 * torch.exp(0.5 * randn(R))
+        s["b_scale"] = torch.exp(0.2 * randn(E, N)) / (36.0 * math.sqrt(K))
+        rs = np.random.RandomState(int(seed) % (1 << 32))
+        p = 1.0 / np.arange(1, E + 1) ** 1.2 if case["skew"] else np.ones(E)
+        counts = rs.multinomial(R, rs.permutation(p / p.sum()))
+        s["counts"] = [int(c) for c in counts]
+        s["m_indptr"] = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32,
+                                     device="cuda")
+        s["out_buf"] = _empty(R, N // 2 if case["gated"] else N,
+                              dtype=torch.bfloat16 if case["out"] == "bf16" else torch.float32)
+    torch.cuda.current_stream().synchronize()
+    return s
+
+
+# ------------------------------------------------------------------ plain forms
+def _route(ids, E):
+    """Stable grouping of the pairs by expert: (m_indptr, perm, inv_perm)."""
+    flat = ids.reshape(-1).long()
+    perm = torch.sort(flat, stable=True).indices
+    inv = torch.empty_like(perm)
+    inv[perm] = torch.arange(perm.numel(), device=perm.device)
+    edges = torch.cumsum((flat[:, None] == torch.arange(E, device=flat.device)).sum(0), 0)
+    m = torch.cat([torch.zeros(1, dtype=edges.dtype, device=edges.device), edges])
+    return m.to(torch.int32), perm.to(torch.int32), inv.to(torch.int32)
+
+
+def _plain_router(s):
+    T, E, k = s["T"], s["E"], s["k"]
+    x = s["logits"].double()   # 64 bits: the choice is between values that may lie close
+    score = torch.sigmoid(x) if s["scoring"] == "sigmoid" else torch.softmax(x, 1)
+    # without a bias the experts' order is the logits' own
+    choice = score + s["bias"].double() if s["bias"] is not None else x
+    if s["n_group"] > 1:
+        by = (score if s["bias"] is None and s["group_top"] > 1 else choice).view(
+            T, s["n_group"], E // s["n_group"])
+        top = by.sort(2, descending=True).values[:, :, :s["group_top"]].sum(2)
+        best = torch.sort(top, dim=1, descending=True, stable=True).indices[:, :s["topk_group"]]
+        keep = torch.zeros(T, s["n_group"], dtype=torch.bool, device=x.device).scatter_(1, best, True)
+        choice = choice.masked_fill(~keep.repeat_interleave(E // s["n_group"], 1), -math.inf)
+    ids = torch.sort(choice, dim=1, descending=True, stable=True).indices[:, :k]
+    w = score.gather(1, ids)
+    if s["renorm"]:
+        w = w / w.sum(1, keepdim=True)
+    got = {"ids": ids.to(torch.int32), "w": (w * s["scale"]).float()}
+    if s["route"]:
+        got["m_indptr"], got["perm"], got["inv_perm"] = _route(ids, E)
+    return got
+
+
+def _plain_norm(s):
+    T, H = s["T"], s["H"]
+    h = s["x"]
+    got = {}
+    if s["residual"] is not None:
+        h = (h.float() + s["residual"].float()).to(torch.bfloat16)
+        got["h"] = h
+    # the mean square in 64 bits: the 8-bit codes next to a rounding border depend on it
+    r = 1.0 / torch.sqrt(h.double().square().sum(1, keepdim=True) / H + s["eps"])
+    y = h.float() * r.float() * s["weight"].float()
+    if s["y"] is not None:
+        got["y"] = y.to(torch.bfloat16)
+    if s["fmt"] == "fp8":
+        b = y.view(T, H // 128, 128)
+        amax = b.abs().amax(2)
+        zero = amax < TINY
+        scale = torch.where(zero, 1.0, amax / 448.0)
+        codes = b * torch.where(zero, 0.0, 448.0 / amax)[:, :, None]
+        got["q"] = codes.clamp(-448, 448).view(T, H).to(torch.float8_e4m3fn)
+        got["q_scale"] = scale.t().contiguous() if s["major"] == "MN" else scale
+    elif s["fmt"] == "mxfp8":
+        b = y.view(T, H // 32, 32)
+        m, e = torch.frexp(b.abs().amax(2))      # amax = m 2^e, m in [0.5, 1)
+        e = (e - 9 + (m > 0.875)).clamp(-127, 127)   # smallest e with amax <= 448 2^e
+        e = torch.where(m == 0, torch.full_like(e, -127), e)
+        got["q"] = torch.ldexp(b, -e[:, :, None]).view(T, H).to(torch.float8_e4m3fn)
+        code = (e + 127).to(torch.uint8)
+        if s["major"] == "MN":
+            code = code.view(T, H // 128, 4).transpose(0, 1).contiguous()
+        got["q_scale"] = code.view(torch.float8_e8m0fnu)
+    elif s["fmt"] == "int8":
+        got["q"], got["q_scale"] = _plain_int8(y)
+    return got
+
+
+def _plain_int8(y):
+    amax = y.abs().amax(1)
+    zero = amax < TINY
+    codes = torch.round(y * torch.where(zero, 0.0, 127.0 / amax)[:, None])
+    return codes.to(torch.int8), torch.where(zero, 1.0, amax / 127.0)
+
+
+def _plain_quantize(s):
+    q, scale = _plain_int8(s["x"].float())
+    if s["inv_perm"] is not None:
+        T, k = s["T"], s["k"]
+        at = s["inv_perm"].long()
+        rows = torch.empty(T * k, s["K"], dtype=q.dtype, device=q.device)
+        rows[at] = q.repeat_interleave(k, 0)
+        scales = torch.empty(T * k, device=q.device)
+        scales[at] = scale.repeat_interleave(k)
+        q, scale = rows, scales
+    return {"q": q, "q_scale": scale}
+
+
+def _silu_mul(v):
+    gate, up = v.chunk(2, 1)
+    return gate / (1.0 + torch.exp(-gate)) * up
+
+
+def _plain_gemm(s):
+    parts, r = [], 0
+    for e, c in enumerate(s["counts"]):
+        if c:
+            v = torch.matmul(s["a"][r:r + c].float(), s["b"][e].float().t())
+            v = v * s["a_scale"][r:r + c, None] * s["b_scale"][e]
+            parts.append((_silu_mul(v) if s["gated"] else v).to(s["out_buf"].dtype))
+            r += c
+    return {"out": torch.cat(parts)}
+
+
+# ------------------------------------------------------------------ the library's calls
+def _own(s):
+    import fp8_block_scaled_route_b200 as moe
+    if s["op"] == "router":
+        how = dict(bias=s["bias"], scoring=s["scoring"], n_group=s["n_group"],
+                   topk_group=s["topk_group"], group_top=s["group_top"], renorm=s["renorm"],
+                   scale=s["scale"])
+        if s["route"]:
+            moe.moe_router_score_route(s["logits"], s["ids"], s["w"], s["m_indptr"], s["perm"],
+                                       s["inv_perm"], s["ws"], **how)
+            return {n: s[n] for n in ("ids", "w", "m_indptr", "perm", "inv_perm")}
+        moe.moe_router_score_topk(s["logits"], s["ids"], s["w"], **how)
+        return {"ids": s["ids"], "w": s["w"]}
+    if s["op"] == "norm":
+        moe.moe_rmsnorm_quant(s["x"], s["weight"], s["eps"], residual=s["residual"],
+                              residual_out=s["h"], y=s["y"], q_format=s["fmt"], q=s["q"],
+                              q_scale=s["q_scale"], scale_major=s["major"])
+        got = {n: s[n] for n in ("h", "y", "q", "q_scale") if s[n] is not None}
+        if s["fmt"] == "mxfp8":
+            got["q_scale"] = got["q_scale"].view(torch.float8_e8m0fnu)
+        return got
+    if s["op"] == "quantize":
+        moe.int8_quantize(s["x"], s["q"], s["q_scale"], inv_perm=s["inv_perm"], k=s["k"])
+        return {"q": s["q"], "q_scale": s["q_scale"]}
+    moe.int8_moe_gemm(s["a"], s["b"], s["a_scale"], s["b_scale"], s["out_buf"],
+                      m_indptr=s["m_indptr"] if s["E"] > 1 else None, is_gated=s["gated"])
+    return {"out": s["out_buf"]}
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"router": _plain_router, "norm": _plain_norm, "quantize": _plain_quantize,
+            "gemm": _plain_gemm}[state["op"]](state)
+
+
+# ------------------------------------------------------------------ bytes and operations
+def work(case):
+    if case["op"] == "router":
+        T, E, k = case["T"], case["E"], case["k"]
+        b = T * E * (4 if case["dtype"] == "f32" else 2) + 8 * T * k + (4 * E if case["bias"] else 0)
+        if case["route"]:
+            b += 8 * T * k + 4 * (E + 1)
+        return {"bytes": b, "flops": 4 * T * E}
+    if case["op"] == "norm":
+        T, H = case["T"], case["H"]
+        b = 2 * T * H * (3 if case["residual"] else 1) + (2 * T * H if case["y"] else 0)
+        b += H * (4 if case["wdtype"] == "f32" else 2)
+        b += {"none": 0, "fp8": T * H + T * H // 32, "mxfp8": T * H + T * H // 32,
+              "int8": T * H + 4 * T}[case["fmt"]]
+        return {"bytes": b, "flops": 6 * T * H}
+    if case["op"] == "quantize":
+        T, K, k = case["T"], case["K"], case["k"]
+        return {"bytes": 2 * T * K + T * k * (K + 4) + (4 * T * k if k > 1 else 0),
+                "flops": 3 * T * K}
+    R, N, K, E = case["R"], case["N"], case["K"], case["E"]
+    n_out = N // 2 if case["gated"] else N
+    touched = min(E, R)
+    b = R * K + touched * N * K + 4 * R + 4 * touched * N + R * n_out * (2 if case["out"] == "bf16" else 4)
+    return {"bytes": b, "flops": 2 * R * N * K}
+
+
+# ------------------------------------------------------------------ 64-bit results
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["op"] == "router":
+        # every expert's selection value by the definitions exp(x) / sum and 1 / (1 + exp(-x))
+        x = s["logits"].to(torch.float64)
+        if case["scoring"] == "softmax":
+            z = torch.exp(x - x.max(1, keepdim=True).values)
+            p = z / z.sum(1, keepdim=True)
+        else:
+            p = 1.0 / (1.0 + torch.exp(-x))
+        sel = p if s["bias"] is None else p + s["bias"].to(torch.float64)[None]
+        T, E, G = case["T"], case["E"], case["n_group"]
+        if G > 1:
+            tops = torch.topk(sel.reshape(T, G, E // G), case["group_top"], dim=2).values.sum(2)
+            place = torch.argsort(torch.argsort(-tops, dim=1, stable=True), dim=1)
+            sel = torch.where((place < case["topk_group"])[:, :, None], sel.reshape(T, G, E // G),
+                              torch.tensor(-math.inf, dtype=torch.float64, device="cuda")).reshape(T, E)
+        at = torch.argsort(-sel, dim=1, stable=True)[:, :case["k"]]
+        w = torch.gather(p, 1, at)
+        w = w * (case["scale"] / w.sum(1, keepdim=True) if case["renorm"] else case["scale"])
+        got = {"ids": None, "w": w}
+        if case["route"]:
+            got.update(m_indptr=None, perm=None, inv_perm=None)
+        return got
+    if case["op"] == "norm":
+        h = s["x"].to(torch.float64)
+        got = {}
+        if s["residual"] is not None:
+            # the residual that is stored, and normalised, is the bf16 one
+            h = h + s["residual"].to(torch.float64)
+            got["h"] = h
+            h = h.to(torch.float32).to(torch.bfloat16).to(torch.float64)
+        y = h * torch.rsqrt(torch.mean(h * h, dim=1, keepdim=True) + s["eps"])
+        y = y * s["weight"].to(torch.float64)
+        if case["y"]:
+            got["y"] = y
+        T, H = case["T"], case["H"]
+        if case["fmt"] == "fp8":
+            sc = torch.amax(torch.abs(y.reshape(T, -1, 128)), dim=2) / 448.0
+            got["q"] = (y.reshape(T, -1, 128) / sc[:, :, None]).reshape(T, H)
+            got["q_scale"] = sc.T.contiguous() if case["major"] == "MN" else sc
+        elif case["fmt"] == "mxfp8":
+            sc = torch.exp2(torch.ceil(torch.log2(torch.amax(torch.abs(y.reshape(T, -1, 32)), dim=2) / 448.0)))
+            got["q"] = (y.reshape(T, -1, 32) / sc[:, :, None]).reshape(T, H)
+            got["q_scale"] = (sc.reshape(T, H // 128, 4).permute(1, 0, 2).contiguous()
+                              if case["major"] == "MN" else sc)
+        elif case["fmt"] == "int8":
+            got["q"] = None
+            got["q_scale"] = torch.amax(torch.abs(y), dim=1) / 127.0
+        return got
+    if case["op"] == "quantize":
+        x = s["x"].to(torch.float64)
+        sc = torch.amax(torch.abs(x), dim=1) / 127.0
+        if s["inv_perm"] is not None:
+            rows = torch.argsort(s["inv_perm"])          # grouped row -> pair
+            sc = sc[rows // case["k"]]
+        return {"q": None, "q_scale": sc}
+    out = torch.empty(s["out_buf"].shape, dtype=torch.float64, device="cuda")
+    edge = s["m_indptr"].tolist()
+    for e in range(case["E"]):
+        lo, hi = edge[e], edge[e + 1]
+        if hi > lo:
+            rows = s["a"][lo:hi].to(torch.float64) * s["a_scale"][lo:hi].to(torch.float64)[:, None]
+            v = rows @ (s["b"][e].to(torch.float64) * s["b_scale"][e].to(torch.float64)[:, None]).T
+            if case["gated"]:
+                half = case["N"] // 2
+                v = v[:, :half] * torch.sigmoid(v[:, :half]) * v[:, half:]
+            out[lo:hi] = v
+    return {"out": out}
