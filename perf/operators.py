@@ -202,6 +202,14 @@ def _plain_router(s):
     return got
 
 
+def _scales(amax, top):
+    """(amax / top, top / amax), each one correctly rounded division (a Python
+    number as an operand would turn it into a product with a reciprocal)."""
+    top = torch.full_like(amax, top)
+    zero = amax < TINY
+    return torch.where(zero, 1.0, amax / top), torch.where(zero, 0.0, top / amax)
+
+
 def _plain_norm(s):
     T, H = s["T"], s["H"]
     h = s["x"]
@@ -216,10 +224,8 @@ def _plain_norm(s):
         got["y"] = y.to(torch.bfloat16)
     if s["fmt"] == "fp8":
         b = y.view(T, H // 128, 128)
-        amax = b.abs().amax(2)
-        zero = amax < TINY
-        scale = torch.where(zero, 1.0, amax / 448.0)
-        codes = b * torch.where(zero, 0.0, 448.0 / amax)[:, :, None]
+        scale, inv = _scales(b.abs().amax(2), 448.0)
+        codes = b * inv[:, :, None]
         got["q"] = codes.clamp(-448, 448).view(T, H).to(torch.float8_e4m3fn)
         got["q_scale"] = scale.t().contiguous() if s["major"] == "MN" else scale
     elif s["fmt"] == "mxfp8":
@@ -238,10 +244,8 @@ def _plain_norm(s):
 
 
 def _plain_int8(y):
-    amax = y.abs().amax(1)
-    zero = amax < TINY
-    codes = torch.round(y * torch.where(zero, 0.0, 127.0 / amax)[:, None])
-    return codes.to(torch.int8), torch.where(zero, 1.0, amax / 127.0)
+    scale, inv = _scales(y.abs().amax(1), 127.0)
+    return torch.round(y * inv[:, None]).to(torch.int8), scale
 
 
 def _plain_quantize(s):
