@@ -30,6 +30,8 @@ __all__ = [
     "moe_tactic_clear", "moe_ep_workspace_size", "moe_ep_plan", "moe_ep_pack",
     "moe_fp8_expert_rows_workspace_size", "moe_fp8_expert_rows", "moe_combine", "moe_router_route",
     "moe_set_expert_fusion", "moe_fp8_fused_plan",
+    "moe_router_score_topk", "moe_router_score_route", "moe_rmsnorm_quant", "int8_quantize",
+    "int8_moe_gemm",
     "MOE_FUSION_AUTO", "MOE_FUSION_ON", "MOE_FUSION_OFF",
 ]
 
@@ -60,6 +62,8 @@ EXPORTS = (
     "moe_ep_workspace_size", "moe_ep_plan", "moe_ep_pack", "moe_fp8_expert_rows_workspace_size",
     "moe_fp8_expert_rows", "moe_combine", "moe_router_route", "moe_set_expert_fusion",
     "moe_fp8_fused_plan",
+    "moe_router_score_topk", "moe_router_score_route", "moe_rmsnorm_quant", "int8_quantize",
+    "int8_moe_gemm",
 )
 
 _lib = None
@@ -159,6 +163,18 @@ def lib():
     L.moe_combine.argtypes = [P, P, P, I, I, I, P, P]
     L.moe_router_route.restype = I
     L.moe_router_route.argtypes = [P, I, I, I, P, P, P, P, P, P, Z, P]
+    D = ctypes.c_double
+    score = [P, I, P] + [I] * 8 + [F, P, P]
+    L.moe_router_score_topk.restype = I
+    L.moe_router_score_topk.argtypes = score + [P]
+    L.moe_router_score_route.restype = I
+    L.moe_router_score_route.argtypes = score + [P, P, P, P, Z, P]
+    L.moe_rmsnorm_quant.restype = I
+    L.moe_rmsnorm_quant.argtypes = [P, P, P, I, D, I, I, P, P, I, P, P, I, P]
+    L.int8_quantize.restype = I
+    L.int8_quantize.argtypes = [P, I, I, I, I, P, P, P, P]
+    L.int8_moe_gemm.restype = I
+    L.int8_moe_gemm.argtypes = [P] * 6 + [I] * 6 + [P]
     _lib = L
     return L
 
@@ -510,6 +526,184 @@ def moe_set_stage_events(events) -> int:
 
 def moe_get_device_status(ws=None, *, stream=None) -> int:
     return int(lib().moe_get_device_status(_ptr(ws), _stream(stream)))
+
+
+# ---------------------------------------------------------------- scored router, norm, int8
+_SCORING = {"softmax": 0, "sigmoid": 1}
+_Q_FORMAT = {"none": 0, "fp8": 1, "mxfp8": 2, "int8": 3}
+_MAJOR = {"K": 0, "MN": 1}
+
+
+def _tensors(where, device, *specs):
+    """Checks tensors against (name, tensor, dtype names, shape): raises
+    ValueError for one that the C entry would misread.  None and raw addresses
+    pass."""
+    for name, t, dtypes, shape in specs:
+        if t is None or isinstance(t, int):
+            continue
+        if str(t.dtype)[6:] not in dtypes:
+            raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(dtypes)}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{where}: {name} is not contiguous")
+        if t.device != device:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
+
+
+def _on(device, stream, call):
+    """Runs call(stream pointer) with `device` current."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}, expected a CUDA device")
+    if device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group, group_top,
+                renorm, scale, dims, logits_dtype):
+    if dims is None:
+        T, E = logits.shape
+        k = topk_ids.shape[1]
+        _tensors(where, logits.device, ("logits", logits, ("float32", "bfloat16"), None),
+                 ("topk_ids", topk_ids, ("int32",), (T, k)),
+                 ("topk_w", topk_w, ("float32",), (T, k)), ("bias", bias, ("float32",), (E,)))
+        dtype = 0 if logits.element_size() == 4 else 1
+    else:
+        T, E, k = dims
+        dtype = {"float32": 0, "bfloat16": 1}.get(logits_dtype, logits_dtype)
+    args = (_ptr(logits), dtype, _ptr(bias), T, E, k, _SCORING.get(scoring, scoring), n_group,
+            topk_group, group_top, int(bool(renorm)), scale, _ptr(topk_ids), _ptr(topk_w))
+    return T, E, k, args
+
+
+def moe_router_score_topk(logits, topk_ids, topk_w, *, bias=None, scoring="softmax", n_group=1,
+                          topk_group=1, group_top=1, renorm=True, scale=1.0, dims=None,
+                          logits_dtype="float32", stream=None, check=True) -> int:
+    """logits fp32 or bf16 [T, E], bias fp32 [E] or None -> topk_ids int32
+    [T, k], topk_w fp32 [T, k].  scoring "softmax" or "sigmoid".
+    dims = (T, E, k) and logits_dtype when raw addresses are passed."""
+    where = "moe_router_score_topk"
+    _, _, _, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
+                             group_top, renorm, scale, dims, logits_dtype)
+    if dims is None:
+        st = _on(logits.device, stream, lambda s: lib().moe_router_score_topk(*a, s))
+    else:
+        st = lib().moe_router_score_topk(*a, _stream(stream))
+    return _check(st, where, check)
+
+
+def moe_router_score_route(logits, topk_ids, topk_w, m_indptr, perm, inv_perm, ws, ws_bytes=None, *,
+                           bias=None, scoring="softmax", n_group=1, topk_group=1, group_top=1,
+                           renorm=True, scale=1.0, dims=None, logits_dtype="float32", stream=None,
+                           check=True) -> int:
+    """moe_router_score_topk + moe_route_permute in one call.
+    dims = (T, E, k) and logits_dtype when raw addresses are passed."""
+    where = "moe_router_score_route"
+    T, E, k, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
+                             group_top, renorm, scale, dims, logits_dtype)
+    if ws_bytes is None:
+        ws_bytes = ws.numel() * ws.element_size()
+    a = a + (_ptr(m_indptr), _ptr(perm), _ptr(inv_perm), _ptr(ws), ws_bytes)
+    if dims is None:
+        _tensors(where, logits.device, ("m_indptr", m_indptr, ("int32",), (E + 1,)),
+                 ("perm", perm, ("int32",), (T * k,)), ("inv_perm", inv_perm, ("int32",), (T * k,)),
+                 ("ws", ws, ("uint8",), None))
+        st = _on(logits.device, stream, lambda s: lib().moe_router_score_route(*a, s))
+    else:
+        st = lib().moe_router_score_route(*a, _stream(stream))
+    return _check(st, where, check)
+
+
+def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=None, q_format="none",
+                      q=None, q_scale=None, scale_major="K", dims=None, weight_dtype="float32",
+                      stream=None, check=True) -> int:
+    """x bf16 [T, H], weight fp32 or bf16 [H], residual / residual_out / y bf16
+    [T, H] or None.  q_format "none", "fp8" (q [T, H] 8-bit, q_scale fp32
+    [T, H/128] or, with scale_major "MN", [H/128, T]), "mxfp8" (q_scale uint8
+    [T, H/32] or [H/128, T, 4]) or "int8" (q int8 [T, H], q_scale fp32 [T]).
+    dims = (T, H) and weight_dtype when raw addresses are passed."""
+    where = "moe_rmsnorm_quant"
+    fmt, mn = _Q_FORMAT.get(q_format, q_format), _MAJOR.get(scale_major, scale_major)
+    if dims is None:
+        T, H = x.shape
+        wide = ("bfloat16",)
+        byte = ("int8",) if fmt == 3 else ("float8_e4m3fn", "uint8")
+        shape = {1: (H // 128, T) if mn == 1 else (T, H // 128),
+                 2: (H // 128, T, 4) if mn == 1 else (T, H // 32), 3: (T,)}.get(fmt)
+        _tensors(where, x.device, ("x", x, wide, None), ("residual", residual, wide, (T, H)),
+                 ("weight", weight, ("float32", "bfloat16"), (H,)),
+                 ("residual_out", residual_out, wide, (T, H)), ("y", y, wide, (T, H)))
+        if fmt:
+            _tensors(where, x.device, ("q", q, byte, (T, H)),
+                     ("q_scale", q_scale, ("uint8", "float8_e8m0fnu") if fmt == 2 else ("float32",),
+                      shape))
+        wd = 0 if weight.element_size() == 4 else 1
+    else:
+        T, H = dims
+        wd = {"float32": 0, "bfloat16": 1}.get(weight_dtype, weight_dtype)
+    a = (_ptr(x), _ptr(residual), _ptr(weight), wd, eps, T, H, _ptr(residual_out), _ptr(y), fmt,
+         _ptr(q), _ptr(q_scale), mn)
+    if dims is None:
+        st = _on(x.device, stream, lambda s: lib().moe_rmsnorm_quant(*a, s))
+    else:
+        st = lib().moe_rmsnorm_quant(*a, _stream(stream))
+    return _check(st, where, check)
+
+
+def int8_quantize(x, q, q_scale, *, inv_perm=None, k=1, dims=None, stream=None, check=True) -> int:
+    """x bf16 [T, K] -> q int8 [R, K], q_scale fp32 [R]; row t goes to the rows
+    inv_perm[t*k : (t+1)*k] (row t without inv_perm).  dims = (T, K, R) when
+    raw addresses are passed."""
+    where = "int8_quantize"
+    if dims is None:
+        T, K = x.shape
+        R = q.shape[0]
+        _tensors(where, x.device, ("x", x, ("bfloat16",), None), ("q", q, ("int8",), (R, K)),
+                 ("q_scale", q_scale, ("float32",), (R,)))
+        if inv_perm is not None:
+            _tensors(where, x.device, ("inv_perm", inv_perm.view(-1), ("int32",), (T * k,)))
+    else:
+        T, K, R = dims
+    a = (_ptr(x), T, K, k, R, _ptr(inv_perm), _ptr(q), _ptr(q_scale))
+    if dims is None:
+        st = _on(x.device, stream, lambda s: lib().int8_quantize(*a, s))
+    else:
+        st = lib().int8_quantize(*a, _stream(stream))
+    return _check(st, where, check)
+
+
+def int8_moe_gemm(a, b, a_scale, b_scale, out, *, m_indptr=None, is_gated=False, dims=None,
+                  out_dtype="bfloat16", stream=None, check=True) -> int:
+    """a int8 [R, K], b int8 [E, N, K] ([N, K] without m_indptr), a_scale fp32
+    [R], b_scale fp32 [E, N], m_indptr int32 [E+1] or None (one expert, all
+    rows), out bf16 or fp32 [R, N/2 if gated else N].  dims = (R, N, K, E) and
+    out_dtype when raw addresses are passed."""
+    where = "int8_moe_gemm"
+    if dims is None:
+        R, K = a.shape
+        E, N = b.shape[:2] if b.dim() == 3 else (1, b.shape[0])
+        if b.shape[-1] != K:
+            raise ValueError(f"{where}: a has K = {K}, b has K = {b.shape[-1]}")
+        if b_scale.numel() != E * N:
+            raise ValueError(f"{where}: b_scale has {b_scale.numel()} values, expected {E * N}")
+        _tensors(where, a.device, ("a", a, ("int8",), None), ("b", b, ("int8",), None),
+                 ("a_scale", a_scale, ("float32",), (R,)), ("b_scale", b_scale, ("float32",), None),
+                 ("m_indptr", m_indptr, ("int32",), (E + 1,)),
+                 ("out", out, ("bfloat16", "float32"), (R, N // 2 if is_gated else N)))
+        od = 0 if out.element_size() == 4 else 1
+    else:
+        R, N, K, E = dims
+        od = {"float32": 0, "bfloat16": 1}.get(out_dtype, out_dtype)
+    args = (_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(m_indptr), _ptr(out), od, R, N, K, E,
+            int(bool(is_gated)))
+    if dims is None:
+        st = _on(a.device, stream, lambda s: lib().int8_moe_gemm(*args, s))
+    else:
+        st = lib().int8_moe_gemm(*args, _stream(stream))
+    return _check(st, where, check)
 
 
 # ---------------------------------------------------------------- expert parallelism

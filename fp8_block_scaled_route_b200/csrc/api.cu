@@ -23,6 +23,9 @@ namespace {
 
 // Status word for the entry points that take no workspace.
 __device__ int g_lib_status[kStatusInts];
+// Status word of int8_moe_gemm: only ever set by its kernels, and cleared when
+// it is read, so that a call costs no clearing launch.
+__device__ int g_i8_status[kStatusInts];
 
 std::atomic<unsigned long long> g_timeout_ns{2000000000ull};
 std::atomic<int> g_fusion{MOE_FUSION_AUTO};
@@ -40,6 +43,7 @@ struct DevInfo {
     int sms = 0;
     int major = 0, minor = 0;
     int* lib_status = nullptr;
+    int* i8_status = nullptr;
     bool ok = false;
 };
 
@@ -61,6 +65,8 @@ const DevInfo* dev_info() {
         void* p = nullptr;
         if (cudaGetSymbolAddress(&p, g_lib_status) != cudaSuccess) return nullptr;
         d.lib_status = static_cast<int*>(p);
+        if (cudaGetSymbolAddress(&p, g_i8_status) != cudaSuccess) return nullptr;
+        d.i8_status = static_cast<int*>(p);
         d.ok = true;
     }
     return &d;
@@ -310,6 +316,114 @@ int moe_route_permute(const int32_t* topk_ids, int T, int k, int E, int32_t* m_i
     RouteArgs ra{topk_ids, T, k, E, m_indptr, perm, inv_perm,
                  reinterpret_cast<int32_t*>(base + up256(sizeof(int) * kStatusInts)), status};
     return launch_route_permute(ra, s);
+}
+
+// Argument rules of the scored router; MOE_OK or the error to return.
+static int check_score(const void* logits, int logits_dtype, int T, int E, int k, int scoring,
+                       int n_group, int topk_group, int group_top, float scale, const void* ids,
+                       const void* w) {
+    if (T < 0 || E < 1 || k < 1 || k > E || k > MOE_ROUTER_MAX_K) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+    if (logits_dtype != MOE_DTYPE_F32 && logits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (scoring != MOE_SCORE_SOFTMAX && scoring != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (n_group < 1 || n_group > MOE_ROUTER_MAX_GROUPS || E % n_group) return MOE_ERR_INVALID_ARG;
+    if (topk_group < 1 || topk_group > n_group || (group_top != 1 && group_top != 2))
+        return MOE_ERR_INVALID_ARG;
+    if (k > topk_group * (E / n_group)) return MOE_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || scale > 3.402823466e38f) return MOE_ERR_INVALID_ARG;
+    if (static_cast<long long>(T) * k > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+int moe_router_score_topk(const void* logits, int logits_dtype, const float* bias, int T, int E,
+                          int k, int scoring, int n_group, int topk_group, int group_top,
+                          int renorm, float scale, int32_t* topk_ids, float* topk_w,
+                          moe_stream_t stream) {
+    if (int st = check_score(logits, logits_dtype, T, E, k, scoring, n_group, topk_group, group_top,
+                             scale, topk_ids, topk_w))
+        return st;
+    const DevInfo* d = dev_info();
+    if (int st = check_device(d)) return st;
+    const ScoreArgs a{logits, logits_dtype == MOE_DTYPE_BF16, bias, T, E, k,
+                      scoring == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, renorm ? 1 : 0,
+                      scale, topk_ids, topk_w};
+    return launch_router_score(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_router_score_route(const void* logits, int logits_dtype, const float* bias, int T, int E,
+                           int k, int scoring, int n_group, int topk_group, int group_top,
+                           int renorm, float scale, int32_t* topk_ids, float* topk_w,
+                           int32_t* m_indptr, int32_t* perm, int32_t* inv_perm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+    if (int st = check_score(logits, logits_dtype, T, E, k, scoring, n_group, topk_group, group_top,
+                             scale, topk_ids, topk_w))
+        return st;
+    if (!m_indptr || !ws || (T > 0 && !perm)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < route_ws_bytes(T, k, E) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    const DevInfo* d = dev_info();
+    if (int st = check_device(d)) return st;
+    char* base = static_cast<char*>(ws);
+    int* status = reinterpret_cast<int*>(base);
+    RouteArgs ra{topk_ids, T, k, E, m_indptr, perm, inv_perm,
+                 reinterpret_cast<int32_t*>(base + up256(sizeof(int) * kStatusInts)), status};
+    const ScoreArgs a{logits, logits_dtype == MOE_DTYPE_BF16, bias, T, E, k,
+                      scoring == MOE_SCORE_SIGMOID, n_group, topk_group, group_top, renorm ? 1 : 0,
+                      scale, topk_ids, topk_w};
+    return launch_router_score_route(a, ra, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int moe_rmsnorm_quant(const void* x, const void* residual, const void* weight, int weight_dtype,
+                      double eps, int T, int H, void* residual_out, void* y, int q_format, void* q,
+                      void* q_scale, int scale_major, moe_stream_t stream) {
+    if (T < 0 || H <= 0 || H % 16 || !(eps > 0.0) || !(eps <= 1.0)) return MOE_ERR_INVALID_ARG;
+    if (weight_dtype != MOE_DTYPE_F32 && weight_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (q_format < MOE_Q_NONE || q_format > MOE_Q_INT8) return MOE_ERR_INVALID_ARG;
+    if (scale_major != 0 && scale_major != 1) return MOE_ERR_INVALID_ARG;
+    if ((q_format == MOE_Q_FP8 || q_format == MOE_Q_MXFP8) && H % 128) return MOE_ERR_INVALID_ARG;
+    if (H > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
+    if (residual_out && !residual) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && !y && q_format == MOE_Q_NONE) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!x || !weight)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && q_format != MOE_Q_NONE && (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+        !aligned16(y) || !aligned16(q) || (reinterpret_cast<uintptr_t>(q_scale) & 3))
+        return MOE_ERR_INVALID_ARG;
+    const DevInfo* d = dev_info();
+    if (int st = check_device(d)) return st;
+    const RmsNormArgs p{x, residual, weight, weight_dtype == MOE_DTYPE_BF16, eps, T, H,
+                        residual_out, y, q_format, scale_major, q, q_scale};
+    return launch_rmsnorm(p, d->sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int int8_quantize(const void* x, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
+                  float* q_scale, moe_stream_t stream) {
+    if (T < 0 || K <= 0 || K % 16 || k < 1 || R < 0) return MOE_ERR_INVALID_ARG;
+    if (!inv_perm && (k != 1 || R < T)) return MOE_ERR_INVALID_ARG;
+    if (K > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
+    if (T > 0 && (!x || (R > 0 && (!q || !q_scale)))) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    const DevInfo* d = dev_info();
+    if (int st = check_device(d)) return st;
+    return launch_int8_quant(x, T, K, k, R, inv_perm, q, q_scale, d->sms,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+int int8_moe_gemm(const int8_t* a, const int8_t* b, const float* a_scale, const float* b_scale,
+                  const int32_t* m_indptr, void* out, int out_dtype, int R, int N, int K, int E,
+                  int is_gated, moe_stream_t stream) {
+    if (R < 0 || N <= 0 || K <= 0 || E < 1 || K % 16 || (is_gated && N % 2)) return MOE_ERR_INVALID_ARG;
+    if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+    if (!m_indptr && E != 1) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || K > MOE_INT8_MAX_K) return MOE_ERR_UNSUPPORTED;
+    if (static_cast<long long>(E) * N > 0x7ffffe00ll || R > 0x7ffffe00) return MOE_ERR_UNSUPPORTED;
+    if (R > 0 && (!a || !b || !a_scale || !b_scale || !out)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+    const DevInfo* d = dev_info();
+    if (int st = check_device(d)) return st;
+    const I8GemmArgs g{a, b, a_scale, b_scale, m_indptr, out, out_dtype == MOE_DTYPE_BF16, R, N, K, E,
+                       is_gated ? 1 : 0, d->i8_status, g_timeout_ns.load(), d->sms};
+    return launch_int8_gemm(g, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t moe_workspace_size(int T, int H, int I, int E, int k) {
@@ -1094,6 +1208,12 @@ int moe_get_device_status(const void* ws, moe_stream_t stream) {
     int h[kStatusInts] = {0, 0, 0, 0};
     const void* src = ws ? ws : d->lib_status;
     if (cudaMemcpy(h, src, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!ws && h[0] == MOE_OK) {
+        if (cudaMemcpy(h, d->i8_status, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        if (h[0] != MOE_OK && cudaMemset(d->i8_status, 0, sizeof(h)) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
     return h[0];
 }
 

@@ -1,0 +1,380 @@
+// Grouped int8 GEMM with a scale per row and per output channel.
+//
+//   S[r, n] = sum_k a[r, k] * b[e, n, k]          (exact, 32-bit integers)
+//   G[r, n] = (float(S) * a_scale[r]) * b_scale[e, n]
+//   out     = G, or gated silu(G[:, :N/2]) * G[:, N/2:], rounded once
+// for rows r of expert e ([m_indptr[e], m_indptr[e+1])).  tcgen05.mma kind::i8
+// sums the whole K range in tensor memory, so no scale is applied inside the
+// main loop and integer partial sums of a split K range add up exactly in any
+// order.
+//
+// Orientation: the weights are the MMA's M operand (128 tensor-memory lanes =
+// 128 weight rows), the token rows its N operand, whose size is an argument
+// of the instruction: an expert with 5 rows costs an N = 16 MMA and a 16-row
+// load.  A warp's 32 lanes are 32 consecutive output channels of one token
+// row, so plain stores are whole 32-byte sectors without a transpose.  Gated:
+// the 128 lanes are granules of 16 gate rows and the 16 up rows that belong to
+// them, so lanes l and l + 16 of a warp hold one output's two halves.
+#include <cuda_bf16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kKB = 128;             // K bytes per stage
+constexpr int kWRows = 128;          // weight rows per CTA tile
+constexpr int kWBytes = kWRows * kKB;
+constexpr int kGran = 16;            // rows per TMA box
+constexpr int kBoxBytes = kGran * kKB;
+constexpr int kThreads = 192;        // warps: 0 TMA, 1 MMA, 2-5 epilogue
+constexpr int kEpiWarps = 4;
+
+struct I8Params {
+    const float* a_scale;
+    const float* b_scale;
+    const int32_t* m_indptr;
+    void* out;
+    int R, N, K, nkb, gated, out_bf16;
+    int* status;
+    unsigned long long timeout_ns;
+};
+
+// Rows of expert e, clamped to [0, R].
+__device__ __forceinline__ void expert_rows(const I8Params& p, int e, int& lo, int& hi) {
+    lo = 0;
+    hi = p.R;
+    if (p.m_indptr) {
+        lo = min(max(p.m_indptr[e], 0), p.R);
+        hi = min(max(p.m_indptr[e + 1], lo), p.R);
+    }
+}
+
+__device__ __forceinline__ void store_out(const I8Params& p, long long at, float v) {
+    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
+    else static_cast<float*>(p.out)[at] = v;
+}
+
+// Output of NC token columns: s[j] is the integer sum of token row row0 + j
+// and this lane's weight row (lane position `pos` of the 128-row tile).  Rows
+// at or past hi are not stored.  Called by whole warps.
+template <int NC>
+__device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], int e, int wt, int pos,
+                                     int row0, int hi) {
+    const int lane = threadIdx.x & 31;
+    const float as_l = lane < NC && row0 + lane < hi ? p.a_scale[row0 + lane] : 0.0f;
+    if (!p.gated) {
+        const int n = wt * kWRows + pos;
+        const bool ok = n < p.N;
+        const float bs = ok ? p.b_scale[static_cast<long long>(e) * p.N + n] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const float as = __shfl_sync(0xffffffffu, as_l, j);
+            if (ok && row0 + j < hi)
+                store_out(p, static_cast<long long>(row0 + j) * p.N + n,
+                          __int2float_rn(s[j]) * as * bs);
+        }
+    } else {
+        const int half = p.N >> 1;
+        const int ch = wt * (kWRows / 2) + (pos >> 5) * kGran + (pos & 15);
+        const bool up = (lane & 16) != 0;
+        const bool ok = ch < half;
+        const float bs = ok ? p.b_scale[static_cast<long long>(e) * p.N + (up ? half : 0) + ch] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+            // the gate lane finishes token j, the up lane token j + 1
+            const float f0 = __int2float_rn(s[j]) * __shfl_sync(0xffffffffu, as_l, j) * bs;
+            const float f1 = __int2float_rn(s[j + 1]) * __shfl_sync(0xffffffffu, as_l, j + 1) * bs;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
+            const float g = up ? got : f0, u = up ? f1 : got;
+            const int row = row0 + j + (up ? 1 : 0);
+            if (ok && row < hi) store_out(p, static_cast<long long>(row) * half + ch, silu_fast(g) * u);
+        }
+    }
+}
+
+// ------------------------------------------------------------ narrow kernel
+// One CTA per (128 weight rows, expert, token block stride z): for each of its
+// blocks of up to BT token rows, the whole K range (or, with a cluster of S
+// CTAs, the S-th part of it) streams through a ring of NST stages.
+template <int BT>
+struct Narrow {
+    static constexpr int NST = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 3;
+    static constexpr int STAGE = kWBytes + BT * kKB;
+    static constexpr int COLS = 2 * BT < 32 ? 32 : 2 * BT;   // two accumulators
+    static constexpr int SMEM = 1024 + NST * STAGE + 256;
+};
+
+template <int BT>
+__global__ void __launch_bounds__(kThreads)
+    int8_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                       const I8Params p, const int S) {
+    using C = Narrow<BT>;
+    extern __shared__ uint8_t smem_raw[];
+    const int e = blockIdx.y;
+    const int wt = S == 1 ? blockIdx.x : blockIdx.x / S;
+    const int ks = S == 1 ? 0 : blockIdx.x - wt * S;
+    int lo, hi;
+    expert_rows(p, e, lo, hi);
+    const int blocks = (hi - lo + BT - 1) / BT;
+    if (static_cast<int>(blockIdx.z) >= blocks) return;  // the whole cluster, if any
+
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE);
+    uint64_t* empty = full + C::NST;
+    uint64_t* tfull = empty + C::NST;    // [2]
+    uint64_t* tempty = tfull + 2;        // [2]
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_s + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kEpiWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_s = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_s, C::COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    const WaitCtl wc{abort_s, p.status, p.timeout_ns};
+    const int kb0 = static_cast<int>(static_cast<long long>(p.nkb) * ks / S);
+    const int kb1 = static_cast<int>(static_cast<long long>(p.nkb) * (ks + 1) / S);
+
+    if (warp == 0) {
+        // lanes 0-7: the tile's eight 16-row weight boxes; lanes 8..: token boxes
+        int wrow = 0;
+        if (lane < 8) {
+            if (!p.gated) {
+                wrow = e * p.N + wt * kWRows + lane * kGran;
+            } else {
+                const int ch = wt * (kWRows / 2) + (lane >> 1) * kGran;
+                wrow = e * p.N + ((lane & 1) ? (p.N >> 1) : 0) + ch;
+            }
+        }
+        uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
+        bool ok = true;
+        for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z) {
+            const int row0 = lo + tb * BT;
+            const int boxes = (min(BT, hi - row0) + kGran - 1) / kGran;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
+                uint8_t* st = base + stage * C::STAGE;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], (8 + boxes) * kBoxBytes);
+                __syncwarp();
+                if (lane < 8)
+                    tma_load_2d(st + lane * kBoxBytes, &tmW, &full[stage], kb * kKB, wrow);
+                else if (lane < 8 + boxes)
+                    tma_load_2d(st + lane * kBoxBytes, &tmX, &full[stage], kb * kKB,
+                                row0 + (lane - 8) * kGran);
+                __syncwarp();
+                armed |= 1u << stage;
+                armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::NST) { stage = 0; phase ^= 1; }
+            }
+        }
+        for (int st = 0; st < C::NST; ++st)
+            if ((armed >> st) & 1u) wait_bar(&full[st], (armed_par >> st) & 1u, wc, 2, /*drain=*/true);
+        __syncwarp();
+    } else if (warp == 1) {
+        uint32_t stage = 0, phase = 0, it = 0;
+        bool ok = true;
+        for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z, ++it) {
+            const int rows = min(BT, hi - (lo + tb * BT));
+            const uint32_t idesc = idesc_s8_s32(kWRows, (rows + 15) & ~15);
+            const uint32_t acc = tmem + (it & 1) * BT;
+            if (!warp_wait_spin(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
+            tc_fence_after();
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!warp_wait_spin(&full[stage], phase, wc, 4)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t sw = smem_u32(base + stage * C::STAGE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_i8(acc, smem_desc_k_sw128(sw + kk * 32),
+                                smem_desc_k_sw128(sw + kWBytes + kk * 32), idesc, kb > kb0 || kk > 0);
+                    umma_commit(&empty[stage]);
+                    if (kb == kb1 - 1) umma_commit(&tfull[it & 1]);
+                }
+                __syncwarp();
+                if (++stage == C::NST) { stage = 0; phase ^= 1; }
+            }
+        }
+        if (elect_one()) umma_commit(drain);
+        __syncwarp();
+        wait_bar(drain, 0, wc, 5, /*drain=*/true);
+        __syncwarp();
+    } else {
+        const int q = warp & 3;
+        const int pos = q * 32 + lane;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        uint32_t it = 0;
+        for (int tb = blockIdx.z; tb < blocks; tb += gridDim.z, ++it) {
+            const int row0 = lo + tb * BT;
+            const int nt = (min(BT, hi - row0) + 15) & ~15;
+            if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
+            tc_fence_after();
+            const uint32_t acc = lane_addr + (it & 1) * BT;
+            if (S == 1) {
+                for (int c = 0; c < nt; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_async(acc + c, v);
+                    tmem_wait_ld(v);
+                    if (c + 16 >= nt) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[it & 1]);
+                    }
+                    int s[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = static_cast<int>(v[j]);
+                    emit<16>(p, s, e, wt, pos, row0 + c, hi);
+                }
+            } else {
+                // one block per CTA: its partial sums go to shared memory, column by
+                // column (the pipeline's stages are free: every MMA has completed)
+                int* part = reinterpret_cast<int*>(base);
+                for (int c = 0; c < nt; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_async(acc + c, v);
+                    tmem_wait_ld(v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * kWRows + pos] = static_cast<int>(v[j]);
+                }
+            }
+        }
+    }
+    if (S > 1) {
+        // every thread of the cluster: partial sums visible, then pair columns
+        // (2i, 2i + 1) are added up and written by CTA i mod S
+        __syncwarp();
+        cluster_sync_all();
+        if (warp >= 2 && !*abort_s) {
+            const int pos = (warp & 3) * 32 + lane;
+            const int row0 = lo + static_cast<int>(blockIdx.z) * BT;
+            const int nt = min(BT, hi - row0);
+            const uint32_t mine = smem_u32(base) + pos * 4;
+            for (int c = 2 * ks; c < nt; c += 2 * S) {
+                int s[2] = {0, 0};
+                for (int r = 0; r < S; ++r) {
+                    const uint32_t at = mapa_shared(mine, r);
+                    s[0] += ld_shared_cluster_s32(at + c * kWRows * 4);
+                    s[1] += ld_shared_cluster_s32(at + (c + 1) * kWRows * 4);
+                }
+                emit<2>(p, s, e, wt, pos, row0 + c, hi);
+            }
+        }
+        __syncwarp();
+        cluster_sync_all();   // peers have read this CTA's sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, C::COLS);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+// 2-D map of a row-major int8 matrix [rows, cols] with 16-row x 128-byte boxes
+// and the 128-byte swizzle; bytes past either end read 0.
+bool make_map(CUtensorMap* m, const void* ptr, long long rows, int cols, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(kKB), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t es[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BT>
+int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int E, int S,
+                  int z, cudaStream_t stream) {
+    using C = Narrow<BT>;
+    static std::atomic<int> ready_dev{-1};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ST_CUDA;
+    if (ready_dev.load() != dev) {
+        if (cudaFuncSetAttribute(int8_narrow_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::SMEM) != cudaSuccess)
+            return ST_CUDA;
+        ready_dev.store(dev);
+    }
+    const int n_rows = p.N;  // weight rows per expert; gated tiles hold 64 + 64 of them
+    const int tiles = p.gated ? (n_rows / 2 + 63) / 64 : (n_rows + 127) / 128;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(tiles * S, E, z);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = S;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = S > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, int8_narrow_kernel<BT>, mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+}
+
+}  // namespace
+
+int launch_int8_gemm(const I8GemmArgs& g, cudaStream_t stream) {
+    if (g.R == 0) return ST_OK;
+    CUtensorMap mw, mx;
+    if (!make_map(&mw, g.b, static_cast<long long>(g.E) * g.N, g.K, kGran) ||
+        !make_map(&mx, g.a, g.R, g.K, kGran))
+        return ST_CUDA;
+    const int nkb = (g.K + kKB - 1) / kKB;
+    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, nkb, g.gated, g.out_bf16,
+                     g.status, g.timeout_ns};
+    const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
+    const int bt = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+    const int z = std::min((per + bt - 1) / bt, 65535);
+    switch (bt) {
+        case 16: return launch_narrow<16>(mw, mx, p, g.E, 1, z, stream);
+        case 32: return launch_narrow<32>(mw, mx, p, g.E, 1, z, stream);
+        case 64: return launch_narrow<64>(mw, mx, p, g.E, 1, z, stream);
+        default: return launch_narrow<128>(mw, mx, p, g.E, 1, z, stream);
+    }
+}
+
+}  // namespace moe

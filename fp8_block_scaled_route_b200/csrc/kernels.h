@@ -106,6 +106,66 @@ int launch_router_topk(const float* logits, int T, int E, int k, int32_t* ids, f
 // launch_route_permute; one launch for at most 8 chunks of pairs.
 int launch_router_route(const float* logits, const RouteArgs& r, float* w, cudaStream_t stream);
 
+// Scored router: logits fp32 or bf16 [T, E] (+ bias fp32 [E]) -> ids int32
+// [T, k], w fp32 [T, k].  E <= 1024, k <= 32, n_group <= 32 divides E,
+// k <= topk_group * E / n_group.
+struct ScoreArgs {
+    const void* logits;
+    int bf16;              // logits are bf16 (1) or fp32 (0)
+    const float* bias;     // may be null
+    int T, E, k;
+    int sigmoid;           // scores: sigmoid (1) or softmax (0)
+    int n_group, topk_group, group_top;
+    int renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+};
+int launch_router_score(const ScoreArgs& a, cudaStream_t stream);
+// The same, then the grouping of the pairs as launch_route_permute (r.status
+// is cleared first); one launch for few tokens.
+int launch_router_score_route(const ScoreArgs& a, const RouteArgs& r, cudaStream_t stream);
+
+// RMS norm of bf16 rows with optional residual addition, bf16 output and
+// 8-bit rows (norm_quant.cu).
+enum NormQuant : int { NQ_NONE = 0, NQ_FP8 = 1, NQ_MXFP8 = 2, NQ_INT8 = 3 };
+struct RmsNormArgs {
+    const void* x;
+    const void* residual;   // may be null
+    const void* weight;     // fp32 or bf16 [H]
+    int weight_bf16;
+    double eps;
+    int T, H;
+    void* residual_out;     // may be null
+    void* y;                // may be null
+    int fmt;                // NormQuant
+    int scale_mn;
+    void* q;
+    void* q_scale;
+};
+int launch_rmsnorm(const RmsNormArgs& p, int num_sms, cudaStream_t stream);
+
+// bf16 rows -> int8 codes and one fp32 scale per row, at rows
+// inv_perm[t*k + j] of [R, K] (row t when inv_perm is null).
+int launch_int8_quant(const void* x, int T, int K, int k, int R, const int32_t* inv_perm,
+                      int8_t* q, float* q_scale, int num_sms, cudaStream_t stream);
+
+// Grouped int8 GEMM (int8_gemm.cu).
+struct I8GemmArgs {
+    const int8_t* a;          // [R, K]
+    const int8_t* b;          // [E, N, K]
+    const float* a_scale;     // [R]
+    const float* b_scale;     // [E, N]
+    const int32_t* m_indptr;  // [E + 1], or null: E = 1, all rows
+    void* out;                // [R, N] or gated [R, N / 2], bf16 or fp32
+    int out_bf16;
+    int R, N, K, E, gated;
+    int* status;
+    uint64_t timeout_ns;
+    int num_sms;
+};
+int launch_int8_gemm(const I8GemmArgs& g, cudaStream_t stream);
+
 // x [T, H] bf16 -> xq rows inv_perm[t*k + j] of [R, H] (row t*k + j when
 // inv_perm is null), xs [H/128, R];
 // also zeroes out_acc [T, H] when not null.

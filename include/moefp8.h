@@ -135,6 +135,101 @@ MOE_API int moe_router_route(const float* logits, int T, int E, int k, int32_t* 
                              float* topk_w, int32_t* m_indptr, int32_t* perm, int32_t* inv_perm,
                              void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Scored router: expert choice by softmax or sigmoid scores, a selection
+ * bias, expert groups, top-k and renormalised weights (the pages define no
+ * router; this is the common form of routers with balanced experts).  For a
+ * token with logits x:
+ *   p_e = softmax(x)_e over all E experts, or 1 / (1 + exp(-x_e));
+ *   c_e = p_e + bias_e, or with bias = NULL the order of x itself;
+ *   the E experts are n_group consecutive groups of E / n_group; a group's
+ *   value is the sum of its group_top (1 or 2) largest c (without a bias: of
+ *   the largest x, or the two largest p), and the topk_group groups with the
+ *   largest value stay (ties to the lower group);
+ *   topk_ids = the k largest c in those groups, descending, ties to the lower
+ *   expert; topk_w_j = p_j, with renorm divided by the sum of the k p_j, times
+ *   scale.
+ * The choice is the one of 64-bit values of c and of the group values, so it
+ * does not depend on 32-bit rounding; the weights are fp32.
+ * An expert is masked when its logit is NaN or at most the lowest finite
+ * value of its type (so also -infinity), or its bias NaN or at most -FLT_MAX:
+ * it takes no part in softmax and group values, ranks after every other
+ * expert of the chosen groups (by index) and gets weight 0; a token whose
+ * experts are all masked gets weights 0.  A group of masked experts ranks
+ * after every other.  +infinity counts as FLT_MAX.
+ *  logits    device [T, E], fp32 (MOE_DTYPE_F32) or bf16 (MOE_DTYPE_BF16)
+ *  bias      device fp32 [E] or NULL
+ *  scoring   MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
+ *  n_group   1 (no groups) to MOE_ROUTER_MAX_GROUPS, divides E;
+ *            1 <= topk_group <= n_group; k <= topk_group * E / n_group
+ *  renorm    0 or 1;  scale  finite, > 0
+ *  topk_ids  device int32 [T, k] out;  topk_w device fp32 [T, k] out
+ * Limits and errors as for moe_router_topk (k <= MOE_ROUTER_MAX_K,
+ * E <= MOE_MAX_EXPERTS); T = 0 is a no-op. */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+#define MOE_ROUTER_MAX_GROUPS 32
+MOE_API int moe_router_score_topk(const void* logits, int logits_dtype, const float* bias, int T,
+                                  int E, int k, int scoring, int n_group, int topk_group,
+                                  int group_top, int renorm, float scale, int32_t* topk_ids,
+                                  float* topk_w, moe_stream_t stream);
+
+/* moe_router_score_topk and moe_route_permute in one call, as
+ * moe_router_route is for the plain router: topk_ids [T, k], topk_w [T, k],
+ * m_indptr [E+1], perm [T*k], inv_perm [T*k] or NULL, ws of at least
+ * moe_route_workspace_size(T, k, E) bytes.  A single kernel launch for up to
+ * 128 tokens.  With T = 0 m_indptr is all zero. */
+MOE_API int moe_router_score_route(const void* logits, int logits_dtype, const float* bias, int T,
+                                   int E, int k, int scoring, int n_group, int topk_group,
+                                   int group_top, int renorm, float scale, int32_t* topk_ids,
+                                   float* topk_w, int32_t* m_indptr, int32_t* perm,
+                                   int32_t* inv_perm, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Residual addition, RMS norm and 8-bit rows                           */
+/* ------------------------------------------------------------------ */
+
+/* The step before the expert layer in a decoder block, in one pass over the
+ * rows:
+ *   h = bf16(x + residual)  (h = x without a residual)
+ *   y = (h * r) * weight,  r = fp32(1 / sqrt(mean(h^2) + eps)), the mean
+ *       square summed in 64 bits, the products rounded in fp32;
+ *   any of: residual_out = h, y as bf16, q = 8-bit rows of y with scales.
+ * The 8-bit rows are taken from the fp32 y (one rounding).  Formats:
+ *   MOE_Q_FP8    E4M3, scale = amax/448 per 128 columns (fp32);
+ *                scale_major 0: [T, H/128], 1: [H/128, T], as the activation
+ *                scales of fp8_groupwise_moe_gemm
+ *   MOE_Q_MXFP8  E4M3, E8M0 scale per 32 columns by the rule of
+ *                swiglu_mxfp8_quant; scale_major 0: [T, H/32], 1: [H/128, T, 4],
+ *                as the activation scales of mxfp8_moe_gemm
+ *   MOE_Q_INT8   scale = amax/127 per row, fp32 [T], as int8_moe_gemm reads
+ *                (scale_major is not used)
+ * Codes are y times the fp32 reciprocal 448/amax (127/amax), rounded to
+ * nearest even; a group whose amax is below 2^-100 gets scale 1 and codes 0
+ * (MXFP8: the rule of swiglu_mxfp8_quant).  A NaN or infinity in a row makes
+ * that row's y NaN or 0 and its scales NaN (E8M0: code 255).
+ *  x             device bf16 [T, H]
+ *  residual      device bf16 [T, H] or NULL
+ *  weight        device [H], fp32 or bf16 (weight_dtype)
+ *  residual_out  device bf16 [T, H] or NULL; may be `residual` itself (updated
+ *                in place) or x; needs a residual
+ *  y             device bf16 [T, H] or NULL; may be x
+ *  q, q_scale    device, as above; unused with MOE_Q_NONE
+ * 0 < eps <= 1.  H a multiple of 16 (128 with MOE_Q_FP8 and MOE_Q_MXFP8), at
+ * most MOE_NORM_MAX_H (else MOE_ERR_UNSUPPORTED).  At least one of y and q is
+ * written.  T = 0 is a no-op.  Buffers 16-byte aligned (q_scale 4). */
+#define MOE_Q_NONE 0
+#define MOE_Q_FP8 1
+#define MOE_Q_MXFP8 2
+#define MOE_Q_INT8 3
+#define MOE_NORM_MAX_H 32768
+MOE_API int moe_rmsnorm_quant(const void* x, const void* residual, const void* weight,
+                              int weight_dtype, double eps, int T, int H, void* residual_out,
+                              void* y, int q_format, void* q, void* q_scale, int scale_major,
+                              moe_stream_t stream);
+
 /* ------------------------------------------------------------------ */
 /* The fused layer                                                      */
 /* ------------------------------------------------------------------ */
@@ -425,6 +520,51 @@ MOE_API int nvfp4_quantize(const void* x, float gscale, uint8_t* q, uint8_t* sf,
  * `stream`. */
 MOE_API int nvfp4_tile_scales(const uint8_t* sf_rowmajor, uint8_t* sf_tiled, int rows, int K,
                               moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Int8 rows and the grouped int8 GEMM                                  */
+/* ------------------------------------------------------------------ */
+
+/* bf16 rows to int8 with one fp32 scale per row, written to the rows where
+ * int8_moe_gemm wants them (the int8 counterpart of the fused layers'
+ * quantise-and-scatter step):
+ *   scale = amax/127, codes = RNE(x * (127/amax)) in [-127, 127]; a row whose
+ *   amax is below 2^-100 gets scale 1 and codes 0; a NaN or infinity makes the
+ *   scale NaN or infinite and the row's codes 0.
+ *  x         device bf16 [T, K]
+ *  inv_perm  device int32 [T*k]: row t goes to the rows inv_perm[t*k + j],
+ *            j < k, of q and q_scale; entries outside [0, R) are skipped (as
+ *            moe_route_permute's -1).  NULL: row t to row t (k = 1, R >= T)
+ *  q         device int8 [R, K] out;  q_scale device fp32 [R] out
+ * Rows that no entry names are left as they were.  K a multiple of 16, at most
+ * MOE_NORM_MAX_H.  T = 0 is a no-op.  x, q 16-byte aligned. */
+MOE_API int int8_quantize(const void* x, int T, int K, int k, int R, const int32_t* inv_perm,
+                          int8_t* q, float* q_scale, moe_stream_t stream);
+
+/* W8A8 product in 8-bit integers with a scale per token row and per output
+ * channel, in the grouped layout of fp8_groupwise_moe_gemm:
+ *   S[r, n] = sum_k a[r, k] * b[e, n, k] exactly (32-bit integers),
+ *   G[r, n] = (fp32(S) * a_scale[r]) * b_scale[e, n],
+ *   e = the expert with m_indptr[e] <= r < m_indptr[e+1];
+ *   plain: out[r, n] = G[r, n], out [R, N];
+ *   gated: out[r, i] = silu(G[r, i]) * G[r, N/2+i], out [R, N/2].
+ *  a         device int8 [R, K] grouped rows (any value, -128 included)
+ *  b         device int8 [E, N, K]
+ *  a_scale   device fp32 [R];  b_scale device fp32 [E, N]
+ *  m_indptr  device int32 [E+1], m_indptr[0] = 0, non-decreasing,
+ *            m_indptr[E] <= R; NULL: one expert (E = 1) with all R rows, a
+ *            dense product
+ *  out       device, bf16 (MOE_DTYPE_BF16) or fp32 (MOE_DTYPE_F32)
+ * Rows outside [m_indptr[0], m_indptr[E]) are not written.  K a multiple of
+ * 16, at most MOE_INT8_MAX_K (the 32-bit sums cannot overflow); any N (gated:
+ * even); a, b, out 16-byte aligned.  R = 0 is a no-op.  Device timeouts are
+ * read with moe_get_device_status(NULL, stream); unlike the other entry
+ * points' errors, one of this call stays until it is read, and reading it
+ * clears it. */
+#define MOE_INT8_MAX_K 131056
+MOE_API int int8_moe_gemm(const int8_t* a, const int8_t* b, const float* a_scale,
+                          const float* b_scale, const int32_t* m_indptr, void* out, int out_dtype,
+                          int R, int N, int K, int E, int is_gated, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Standalone SwiGLU + MXFP8 quantisation                               */
