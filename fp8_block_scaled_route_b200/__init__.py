@@ -529,54 +529,98 @@ def moe_get_device_status(ws=None, *, stream=None) -> int:
 
 
 # ---------------------------------------------------------------- scored router, norm, int8
+# These calls are a few microseconds of GPU work at decoding sizes, so their
+# marshalling is kept short: checks by identity, addresses as plain integers.
 _SCORING = {"softmax": 0, "sigmoid": 1}
 _Q_FORMAT = {"none": 0, "fp8": 1, "mxfp8": 2, "int8": 3}
 _MAJOR = {"K": 0, "MN": 1}
+_DTYPE = {"float32": 0, "bfloat16": 1}
 
 
-def _tensors(where, device, *specs):
-    """Checks tensors against (name, tensor, dtype names, shape): raises
-    ValueError for one that the C entry would misread.  None and raw addresses
-    pass."""
-    for name, t, dtypes, shape in specs:
-        if t is None or isinstance(t, int):
+class _Torch:
+    """What the checks need of torch, looked up once (on the first call that
+    passes tensors)."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
+        self.i8, self.u8 = torch.int8, torch.uint8
+        self.float = (torch.float32, torch.bfloat16)
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.e8m0 = (torch.uint8, torch.float8_e8m0fnu)
+        self.code = {self.f32: 0, self.bf16: 1}
+        self.current_device = torch.cuda.current_device
+        self.on_device = torch.cuda.device
+        # the current stream's handle without building a Stream object (3 us);
+        # the public way where this torch lacks it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_tc = None
+
+
+def _torch():
+    global _tc
+    if _tc is None:
+        _tc = _Torch()
+    return _tc
+
+
+def _tensors(where, dev, *specs):
+    """Checks tensors against (name, tensor, dtype or dtypes, shape or None):
+    raises ValueError for one that the C entry would misread.  None and raw
+    addresses pass."""
+    for name, t, dtype, shape in specs:
+        if t is None or t.__class__ is int:
             continue
-        if str(t.dtype)[6:] not in dtypes:
-            raise ValueError(f"{where}: {name} is {t.dtype}, expected {' or '.join(dtypes)}")
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        ok = t.dtype in dtype if dtype.__class__ is tuple else t.dtype is dtype
+        if not ok:
+            raise ValueError(f"{where}: {name} is {t.dtype}, expected {dtype}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} is not contiguous")
-        if t.device != device:
-            raise ValueError(f"{where}: {name} is on {t.device}, expected {device}")
+        if t.get_device() != dev:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected CUDA device {dev}")
 
 
-def _on(device, stream, call):
-    """Runs call(stream pointer) with `device` current."""
-    import torch
-    if device.type != "cuda":
-        raise ValueError(f"tensors are on {device}, expected a CUDA device")
-    if device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+def _addr(t):
+    return t if t is None or t.__class__ is int else t.data_ptr()
+
+
+def _call(where, fn, args, dev, stream, check):
+    """fn(*args, stream) with device `dev` current (None: whichever is)."""
+    if dev is None:
+        st = fn(*args, _stream(stream))
+    elif dev < 0:
+        raise ValueError(f"{where}: tensors are not on a CUDA device")
+    elif dev == _tc.current_device():
+        st = fn(*args, _tc.raw_stream(dev) if stream is None else _stream(stream))
+    else:
+        with _tc.on_device(dev):
+            st = fn(*args, _tc.raw_stream(dev) if stream is None else _stream(stream))
+    if check and st != MOE_OK:
+        raise MoEError(st, where)
+    return st
 
 
 def _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group, group_top,
                 renorm, scale, dims, logits_dtype):
     if dims is None:
+        tc = _torch()
         T, E = logits.shape
         k = topk_ids.shape[1]
-        _tensors(where, logits.device, ("logits", logits, ("float32", "bfloat16"), None),
-                 ("topk_ids", topk_ids, ("int32",), (T, k)),
-                 ("topk_w", topk_w, ("float32",), (T, k)), ("bias", bias, ("float32",), (E,)))
-        dtype = 0 if logits.element_size() == 4 else 1
+        dev = logits.get_device()
+        _tensors(where, dev, ("logits", logits, tc.float, None), ("topk_ids", topk_ids, tc.i32, (T, k)),
+                 ("topk_w", topk_w, tc.f32, (T, k)), ("bias", bias, tc.f32, (E,)))
+        dtype = tc.code[logits.dtype]
     else:
         T, E, k = dims
-        dtype = {"float32": 0, "bfloat16": 1}.get(logits_dtype, logits_dtype)
-    args = (_ptr(logits), dtype, _ptr(bias), T, E, k, _SCORING.get(scoring, scoring), n_group,
-            topk_group, group_top, int(bool(renorm)), scale, _ptr(topk_ids), _ptr(topk_w))
-    return T, E, k, args
+        dev, dtype = None, _DTYPE.get(logits_dtype, logits_dtype)
+    return T, E, k, dev, (_addr(logits), dtype, _addr(bias), T, E, k, _SCORING.get(scoring, scoring),
+                          n_group, topk_group, group_top, 1 if renorm else 0, scale, _addr(topk_ids),
+                          _addr(topk_w))
 
 
 def moe_router_score_topk(logits, topk_ids, topk_w, *, bias=None, scoring="softmax", n_group=1,
@@ -586,13 +630,9 @@ def moe_router_score_topk(logits, topk_ids, topk_w, *, bias=None, scoring="softm
     [T, k], topk_w fp32 [T, k].  scoring "softmax" or "sigmoid".
     dims = (T, E, k) and logits_dtype when raw addresses are passed."""
     where = "moe_router_score_topk"
-    _, _, _, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
-                             group_top, renorm, scale, dims, logits_dtype)
-    if dims is None:
-        st = _on(logits.device, stream, lambda s: lib().moe_router_score_topk(*a, s))
-    else:
-        st = lib().moe_router_score_topk(*a, _stream(stream))
-    return _check(st, where, check)
+    _, _, _, dev, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
+                                  group_top, renorm, scale, dims, logits_dtype)
+    return _call(where, lib().moe_router_score_topk, a, dev, stream, check)
 
 
 def moe_router_score_route(logits, topk_ids, topk_w, m_indptr, perm, inv_perm, ws, ws_bytes=None, *,
@@ -602,19 +642,16 @@ def moe_router_score_route(logits, topk_ids, topk_w, m_indptr, perm, inv_perm, w
     """moe_router_score_topk + moe_route_permute in one call.
     dims = (T, E, k) and logits_dtype when raw addresses are passed."""
     where = "moe_router_score_route"
-    T, E, k, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
-                             group_top, renorm, scale, dims, logits_dtype)
+    T, E, k, dev, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
+                                  group_top, renorm, scale, dims, logits_dtype)
+    if dims is None:
+        tc = _torch()
+        _tensors(where, dev, ("m_indptr", m_indptr, tc.i32, (E + 1,)), ("perm", perm, tc.i32, (T * k,)),
+                 ("inv_perm", inv_perm, tc.i32, (T * k,)), ("ws", ws, tc.u8, None))
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size()
-    a = a + (_ptr(m_indptr), _ptr(perm), _ptr(inv_perm), _ptr(ws), ws_bytes)
-    if dims is None:
-        _tensors(where, logits.device, ("m_indptr", m_indptr, ("int32",), (E + 1,)),
-                 ("perm", perm, ("int32",), (T * k,)), ("inv_perm", inv_perm, ("int32",), (T * k,)),
-                 ("ws", ws, ("uint8",), None))
-        st = _on(logits.device, stream, lambda s: lib().moe_router_score_route(*a, s))
-    else:
-        st = lib().moe_router_score_route(*a, _stream(stream))
-    return _check(st, where, check)
+    a += (_addr(m_indptr), _addr(perm), _addr(inv_perm), _addr(ws), ws_bytes)
+    return _call(where, lib().moe_router_score_route, a, dev, stream, check)
 
 
 def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=None, q_format="none",
@@ -628,29 +665,28 @@ def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=Non
     where = "moe_rmsnorm_quant"
     fmt, mn = _Q_FORMAT.get(q_format, q_format), _MAJOR.get(scale_major, scale_major)
     if dims is None:
-        T, H = x.shape
-        wide = ("bfloat16",)
-        byte = ("int8",) if fmt == 3 else ("float8_e4m3fn", "uint8")
-        shape = {1: (H // 128, T) if mn == 1 else (T, H // 128),
-                 2: (H // 128, T, 4) if mn == 1 else (T, H // 32), 3: (T,)}.get(fmt)
-        _tensors(where, x.device, ("x", x, wide, None), ("residual", residual, wide, (T, H)),
-                 ("weight", weight, ("float32", "bfloat16"), (H,)),
-                 ("residual_out", residual_out, wide, (T, H)), ("y", y, wide, (T, H)))
-        if fmt:
-            _tensors(where, x.device, ("q", q, byte, (T, H)),
-                     ("q_scale", q_scale, ("uint8", "float8_e8m0fnu") if fmt == 2 else ("float32",),
-                      shape))
-        wd = 0 if weight.element_size() == 4 else 1
+        tc = _torch()
+        shape = x.shape
+        T, H = shape
+        dev = x.get_device()
+        _tensors(where, dev, ("x", x, tc.bf16, None), ("residual", residual, tc.bf16, shape),
+                 ("weight", weight, tc.float, (H,)), ("residual_out", residual_out, tc.bf16, shape),
+                 ("y", y, tc.bf16, shape))
+        if fmt == 1:
+            _tensors(where, dev, ("q", q, tc.e4m3, shape),
+                     ("q_scale", q_scale, tc.f32, (H // 128, T) if mn == 1 else (T, H // 128)))
+        elif fmt == 2:
+            _tensors(where, dev, ("q", q, tc.e4m3, shape),
+                     ("q_scale", q_scale, tc.e8m0, (H // 128, T, 4) if mn == 1 else (T, H // 32)))
+        elif fmt == 3:
+            _tensors(where, dev, ("q", q, tc.i8, shape), ("q_scale", q_scale, tc.f32, (T,)))
+        wd = tc.code[weight.dtype]
     else:
         T, H = dims
-        wd = {"float32": 0, "bfloat16": 1}.get(weight_dtype, weight_dtype)
-    a = (_ptr(x), _ptr(residual), _ptr(weight), wd, eps, T, H, _ptr(residual_out), _ptr(y), fmt,
-         _ptr(q), _ptr(q_scale), mn)
-    if dims is None:
-        st = _on(x.device, stream, lambda s: lib().moe_rmsnorm_quant(*a, s))
-    else:
-        st = lib().moe_rmsnorm_quant(*a, _stream(stream))
-    return _check(st, where, check)
+        dev, wd = None, _DTYPE.get(weight_dtype, weight_dtype)
+    a = (_addr(x), _addr(residual), _addr(weight), wd, eps, T, H, _addr(residual_out), _addr(y), fmt,
+         _addr(q), _addr(q_scale), mn)
+    return _call(where, lib().moe_rmsnorm_quant, a, dev, stream, check)
 
 
 def int8_quantize(x, q, q_scale, *, inv_perm=None, k=1, dims=None, stream=None, check=True) -> int:
@@ -659,51 +695,46 @@ def int8_quantize(x, q, q_scale, *, inv_perm=None, k=1, dims=None, stream=None, 
     raw addresses are passed."""
     where = "int8_quantize"
     if dims is None:
+        tc = _torch()
         T, K = x.shape
         R = q.shape[0]
-        _tensors(where, x.device, ("x", x, ("bfloat16",), None), ("q", q, ("int8",), (R, K)),
-                 ("q_scale", q_scale, ("float32",), (R,)))
-        if inv_perm is not None:
-            _tensors(where, x.device, ("inv_perm", inv_perm.view(-1), ("int32",), (T * k,)))
+        dev = x.get_device()
+        _tensors(where, dev, ("x", x, tc.bf16, None), ("q", q, tc.i8, (R, K)),
+                 ("q_scale", q_scale, tc.f32, (R,)), ("inv_perm", inv_perm, tc.i32, None))
+        if inv_perm is not None and inv_perm.numel() != T * k:
+            raise ValueError(f"{where}: inv_perm has {inv_perm.numel()} entries, expected {T * k}")
     else:
         T, K, R = dims
-    a = (_ptr(x), T, K, k, R, _ptr(inv_perm), _ptr(q), _ptr(q_scale))
-    if dims is None:
-        st = _on(x.device, stream, lambda s: lib().int8_quantize(*a, s))
-    else:
-        st = lib().int8_quantize(*a, _stream(stream))
-    return _check(st, where, check)
+        dev = None
+    a = (_addr(x), T, K, k, R, _addr(inv_perm), _addr(q), _addr(q_scale))
+    return _call(where, lib().int8_quantize, a, dev, stream, check)
 
 
 def int8_moe_gemm(a, b, a_scale, b_scale, out, *, m_indptr=None, is_gated=False, dims=None,
                   out_dtype="bfloat16", stream=None, check=True) -> int:
-    """a int8 [R, K], b int8 [E, N, K] ([N, K] without m_indptr), a_scale fp32
-    [R], b_scale fp32 [E, N], m_indptr int32 [E+1] or None (one expert, all
-    rows), out bf16 or fp32 [R, N/2 if gated else N].  dims = (R, N, K, E) and
-    out_dtype when raw addresses are passed."""
+    """a int8 [R, K], b int8 [E, N, K] (or [N, K]: one expert), a_scale fp32
+    [R], b_scale fp32 [E, N] (or [N]), m_indptr int32 [E+1] or None (one
+    expert, all rows), out bf16 or fp32 [R, N/2 if gated else N].
+    dims = (R, N, K, E) and out_dtype when raw addresses are passed."""
     where = "int8_moe_gemm"
     if dims is None:
+        tc = _torch()
         R, K = a.shape
-        E, N = b.shape[:2] if b.dim() == 3 else (1, b.shape[0])
-        if b.shape[-1] != K:
-            raise ValueError(f"{where}: a has K = {K}, b has K = {b.shape[-1]}")
-        if b_scale.numel() != E * N:
-            raise ValueError(f"{where}: b_scale has {b_scale.numel()} values, expected {E * N}")
-        _tensors(where, a.device, ("a", a, ("int8",), None), ("b", b, ("int8",), None),
-                 ("a_scale", a_scale, ("float32",), (R,)), ("b_scale", b_scale, ("float32",), None),
-                 ("m_indptr", m_indptr, ("int32",), (E + 1,)),
-                 ("out", out, ("bfloat16", "float32"), (R, N // 2 if is_gated else N)))
-        od = 0 if out.element_size() == 4 else 1
+        bs = b.shape
+        E, N = (bs[0], bs[1]) if len(bs) == 3 else (1, bs[0])
+        dev = a.get_device()
+        _tensors(where, dev, ("a", a, tc.i8, None), ("b", b, tc.i8, (E, N, K) if len(bs) == 3 else (N, K)),
+                 ("a_scale", a_scale, tc.f32, (R,)),
+                 ("b_scale", b_scale, tc.f32, (N,) if b_scale.dim() == 1 and E == 1 else (E, N)),
+                 ("m_indptr", m_indptr, tc.i32, (E + 1,)),
+                 ("out", out, tc.float, (R, N // 2 if is_gated else N)))
+        od = tc.code[out.dtype]
     else:
         R, N, K, E = dims
-        od = {"float32": 0, "bfloat16": 1}.get(out_dtype, out_dtype)
-    args = (_ptr(a), _ptr(b), _ptr(a_scale), _ptr(b_scale), _ptr(m_indptr), _ptr(out), od, R, N, K, E,
-            int(bool(is_gated)))
-    if dims is None:
-        st = _on(a.device, stream, lambda s: lib().int8_moe_gemm(*args, s))
-    else:
-        st = lib().int8_moe_gemm(*args, _stream(stream))
-    return _check(st, where, check)
+        dev, od = None, _DTYPE.get(out_dtype, out_dtype)
+    args = (_addr(a), _addr(b), _addr(a_scale), _addr(b_scale), _addr(m_indptr), _addr(out), od, R, N, K,
+            E, 1 if is_gated else 0)
+    return _call(where, lib().int8_moe_gemm, args, dev, stream, check)
 
 
 # ---------------------------------------------------------------- expert parallelism

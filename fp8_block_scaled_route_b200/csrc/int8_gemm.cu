@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -43,7 +44,7 @@ struct I8Params {
     const float* b_scale;
     const int32_t* m_indptr;
     void* out;
-    int R, N, K, nkb, gated, out_bf16;
+    int R, N, K, E, nkb;
     int* status;
     unsigned long long timeout_ns;
 };
@@ -58,20 +59,21 @@ __device__ __forceinline__ void expert_rows(const I8Params& p, int e, int& lo, i
     }
 }
 
+template <bool BF16>
 __device__ __forceinline__ void store_out(const I8Params& p, long long at, float v) {
-    if (p.out_bf16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
+    if constexpr (BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
     else static_cast<float*>(p.out)[at] = v;
 }
 
 // Output of NC token columns: s[j] is the integer sum of token row row0 + j
 // and this lane's weight row (lane position `pos` of the 128-row tile).  Rows
 // at or past hi are not stored.  Called by whole warps.
-template <int NC>
+template <bool GATED, bool BF16, int NC>
 __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], int e, int wt, int pos,
                                      int row0, int hi) {
     const int lane = threadIdx.x & 31;
     const float as_l = lane < NC && row0 + lane < hi ? p.a_scale[row0 + lane] : 0.0f;
-    if (!p.gated) {
+    if constexpr (!GATED) {
         const int n = wt * kWRows + pos;
         const bool ok = n < p.N;
         const float bs = ok ? p.b_scale[static_cast<long long>(e) * p.N + n] : 0.0f;
@@ -79,7 +81,7 @@ __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], int 
         for (int j = 0; j < NC; ++j) {
             const float as = __shfl_sync(0xffffffffu, as_l, j);
             if (ok && row0 + j < hi)
-                store_out(p, static_cast<long long>(row0 + j) * p.N + n,
+                store_out<BF16>(p, static_cast<long long>(row0 + j) * p.N + n,
                           __int2float_rn(s[j]) * as * bs);
         }
     } else {
@@ -96,7 +98,7 @@ __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], int 
             const float got = __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
             const float g = up ? got : f0, u = up ? f1 : got;
             const int row = row0 + j + (up ? 1 : 0);
-            if (ok && row < hi) store_out(p, static_cast<long long>(row) * half + ch, silu_fast(g) * u);
+            if (ok && row < hi) store_out<BF16>(p, static_cast<long long>(row) * half + ch, silu_fast(g) * u);
         }
     }
 }
@@ -113,8 +115,15 @@ struct Narrow {
     static constexpr int SMEM = 1024 + NST * STAGE + 256;
 };
 
-template <int BT>
-__global__ void __launch_bounds__(kThreads)
+// Global row of weight box i (16 rows) of 128-row tile wt of expert e.
+template <bool GATED>
+__device__ __forceinline__ int weight_box_row(const I8Params& p, int e, int wt, int i) {
+    if constexpr (!GATED) return e * p.N + wt * kWRows + i * kGran;
+    return e * p.N + ((i & 1) ? (p.N >> 1) : 0) + wt * (kWRows / 2) + (i >> 1) * kGran;
+}
+
+template <int BT, bool GATED, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
     int8_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const I8Params p, const int S) {
     using C = Narrow<BT>;
@@ -166,15 +175,7 @@ __global__ void __launch_bounds__(kThreads)
 
     if (warp == 0) {
         // lanes 0-7: the tile's eight 16-row weight boxes; lanes 8..: token boxes
-        int wrow = 0;
-        if (lane < 8) {
-            if (!p.gated) {
-                wrow = e * p.N + wt * kWRows + lane * kGran;
-            } else {
-                const int ch = wt * (kWRows / 2) + (lane >> 1) * kGran;
-                wrow = e * p.N + ((lane & 1) ? (p.N >> 1) : 0) + ch;
-            }
-        }
+        const int wrow = weight_box_row<GATED>(p, e, wt, lane & 7);
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z) {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads)
                     int s[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[j] = static_cast<int>(v[j]);
-                    emit<16>(p, s, e, wt, pos, row0 + c, hi);
+                    emit<GATED, BF16, 16>(p, s, e, wt, pos, row0 + c, hi);
                 }
             } else {
                 // one block per CTA: its partial sums go to shared memory, column by
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads)
                     s[0] += ld_shared_cluster_s32(at + c * kWRows * 4);
                     s[1] += ld_shared_cluster_s32(at + (c + 1) * kWRows * 4);
                 }
-                emit<2>(p, s, e, wt, pos, row0 + c, hi);
+                emit<GATED, BF16, 2>(p, s, e, wt, pos, row0 + c, hi);
             }
         }
         __syncwarp();
@@ -295,6 +296,230 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, C::COLS);
+}
+
+// ------------------------------------------------------------ pair kernel
+// Persistent CTA pairs (cta_group::2), one per two SMs.  A tile is two
+// neighbouring 128-row weight tiles (one per CTA) x up to 256 token rows of
+// one expert; each CTA stages its own weight rows and half of the token rows,
+// so a 128-byte K block costs an SM 32 KB of loads for 512 clocks of MMA, two
+// thirds of what a single-CTA 128 x 256 tile loads.  Two 256-column
+// accumulators in tensor memory let the epilogue of one tile run under the
+// next tile's main loop.
+struct Pair {
+    static constexpr int NST = 6;
+    static constexpr int BT = 256;
+    static constexpr int STAGE = kWBytes + (BT / 2) * kKB;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int MAX_E = 1024;
+    static constexpr int TABLE = ((MAX_E + 1) * 4 + 15) / 16 * 16;
+    static constexpr int SMEM = 1024 + NST * STAGE + TABLE + 256;
+    static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// A wait that also orders the waiting thread after cluster-scope arrivals.
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
+                                                  int where) {
+    const bool ok = warp_wait_spin(bar, parity, wc, where);
+    fence_acq_cluster();
+    return ok;
+}
+
+template <bool GATED, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
+    int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                     const I8Params p) {
+    using C = Pair;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    int* tstart = reinterpret_cast<int*>(base + C::NST * C::STAGE);   // [E + 1] first tile
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE + C::TABLE);
+    uint64_t* empty = full + C::NST;
+    uint64_t* tfull = empty + C::NST;    // [2]
+    uint64_t* tempty = tfull + 2;        // [2], the even CTA's
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_s + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::NST; ++i) {
+            mbar_init(&full[i], 1);      // the even CTA's producer; both CTAs' bytes
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * C::EPI_WARPS);
+        }
+        mbar_init(drain, 1);
+        *abort_s = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_s, 512);
+        tmem_relinquish_pair();
+    }
+    const int wtiles = GATED ? ((p.N >> 1) + 127) >> 7 : (p.N + 255) >> 8;   // of 256 weight rows
+    if (warp == 2) {
+        // first tile of every expert: a lane sums `per` experts, then a scan
+        const int E = p.E;
+        const int per = (E + 31) >> 5;
+        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+        int sum = 0;
+        for (int e = e0; e < e1; ++e) {
+            int lo, hi;
+            expert_rows(p, e, lo, hi);
+            tstart[e] = hi - lo;         // rows, replaced below
+            sum += ((hi - lo + C::BT - 1) / C::BT) * wtiles;
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        int run = incl - sum;
+        for (int e = e0; e < e1; ++e) {
+            const int n = (tstart[e] + C::BT - 1) / C::BT * wtiles;
+            tstart[e] = run;
+            run += n;
+        }
+        if (lane == 31) tstart[E] = incl;
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();    // the peer's barriers and tensor memory are ready
+    tc_fence_after();
+    const uint32_t tmem = *tmem_s;
+    const WaitCtl wc{abort_s, p.status, p.timeout_ns};
+    const int total = tstart[p.E];
+    const int stride = gridDim.x >> 1;
+
+    struct Tile {
+        int e, wt, row0, rows;
+    };
+    // token blocks inner, so that concurrent pairs share weight tiles
+    auto decode = [&](int t) {
+        int lo = 0, hi = p.E;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (tstart[mid] <= t) lo = mid; else hi = mid;
+        }
+        int r0, r1;
+        expert_rows(p, lo, r0, r1);
+        const int local = t - tstart[lo];
+        const int blocks = (r1 - r0 + C::BT - 1) / C::BT;
+        const int w = local / blocks;
+        Tile x;
+        x.e = lo;
+        x.wt = 2 * w + static_cast<int>(rank);
+        x.row0 = r0 + (local - w * blocks) * C::BT;
+        x.rows = min(C::BT, r1 - x.row0);
+        return x;
+    };
+
+    if (warp == 0) {
+        uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
+        bool ok = true;
+        for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
+            const Tile x = decode(t);
+            const int half = ((x.rows + 31) & ~31) >> 1;      // token rows of this CTA
+            const int boxes = half / kGran;
+            const int wrow = weight_box_row<GATED>(p, x.e, x.wt, lane & 7);
+            const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * kGran;
+            for (int kb = 0; kb < p.nkb; ++kb) {
+                if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
+                uint8_t* st = base + stage * C::STAGE;
+                if (rank == 0 && lane == 0)
+                    mbar_arrive_expect_tx(&full[stage], 2 * (8 + boxes) * kBoxBytes);
+                __syncwarp();
+                if (lane < 8)
+                    tma_load_2d_pair(st + lane * kBoxBytes, &tmW, &full[stage], kb * kKB, wrow);
+                else if (lane < 8 + boxes)
+                    tma_load_2d_pair(st + lane * kBoxBytes, &tmX, &full[stage], kb * kKB, xrow);
+                __syncwarp();
+                armed |= 1u << stage;
+                armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
+                if (++stage == C::NST) { stage = 0; phase ^= 1; }
+            }
+        }
+        // No copy and no arrival may still be on its way when the CTA ends.  The
+        // even CTA's barriers count both CTAs' copies; the odd CTA waits until
+        // the MMAs have released its stages.  After an abort one wait runs out
+        // (2 s, long after any copy has landed) and the rest are skipped.
+        uint64_t* last = rank == 0 ? full : empty;
+        for (int st = 0; st < C::NST; ++st)
+            if (((armed >> st) & 1u) &&
+                !wait_bar(&last[st], (armed_par >> st) & 1u, wc, 2, /*drain=*/true))
+                break;
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0) {
+            uint32_t stage = 0, phase = 0, it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x >> 1; t < total && ok; t += stride, ++it) {
+                const Tile x = decode(t);
+                const uint32_t idesc = idesc_s8_s32(2 * kWRows, (x.rows + 31) & ~31);
+                const uint32_t acc = tmem + (it & 1) * C::BT;
+                if (!warp_wait_cluster(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < p.nkb; ++kb) {
+                    if (!warp_wait_spin(&full[stage], phase, wc, 4)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t sw = smem_u32(base + stage * C::STAGE);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_i8_pair(acc, smem_desc_k_sw128(sw + kk * 32),
+                                         smem_desc_k_sw128(sw + kWBytes + kk * 32), idesc, kb > 0 || kk > 0);
+                        umma_commit_pair(&empty[stage]);
+                        if (kb == p.nkb - 1) umma_commit_pair(&tfull[it & 1]);
+                    }
+                    __syncwarp();
+                    if (++stage == C::NST) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (elect_one()) umma_commit_pair_local(drain);
+            __syncwarp();
+            wait_bar(drain, 0, wc, 5, /*drain=*/true);
+            __syncwarp();
+        }
+    } else {
+        const int q = warp & 3;
+        const int part = (warp - 2) >> 2;    // columns [128 part, 128 part + 128)
+        const int pos = q * 32 + lane;
+        const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        uint32_t it = 0;
+        for (int t = blockIdx.x >> 1; t < total; t += stride, ++it) {
+            const Tile x = decode(t);
+            const int hi = x.row0 + x.rows;
+            if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
+            tc_fence_after();
+            const uint32_t acc = lane_addr + (it & 1) * C::BT;
+            for (int c = part * 128; c < min(x.rows, part * 128 + 128); c += 32) {
+                uint32_t v[32];
+                tmem_ld32_async(acc + c, v);
+                tmem_wait_ld(v);
+                int s[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) s[j] = static_cast<int>(v[j]);
+                emit<GATED, BF16, 32>(p, s, x.e, x.wt, pos, x.row0 + c, hi);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(tempty0 + (it & 1) * 8);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync_all();    // both CTAs done with barriers, operands and tensor memory
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -325,23 +550,32 @@ bool make_map(CUtensorMap* m, const void* ptr, long long rows, int cols, int box
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT>
-int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int E, int S,
+// Opt-in of a kernel to its dynamic shared memory, once per device and kernel
+// (`ready_dev` is the kernel's own; alternating devices just set it again).
+template <typename Kern>
+bool smem_ready(Kern kern, int bytes, std::atomic<int>& ready_dev) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (ready_dev.load() == dev) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return false;
+    ready_dev.store(dev);
+    return true;
+}
+
+int weight_tiles(const I8GemmArgs& g) {
+    return g.gated ? (g.N / 2 + 63) / 64 : (g.N + 127) / 128;
+}
+
+template <int BT, bool GATED, bool BF16>
+int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int tiles, int S,
                   int z, cudaStream_t stream) {
     using C = Narrow<BT>;
     static std::atomic<int> ready_dev{-1};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_CUDA;
-    if (ready_dev.load() != dev) {
-        if (cudaFuncSetAttribute(int8_narrow_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::SMEM) != cudaSuccess)
-            return ST_CUDA;
-        ready_dev.store(dev);
-    }
-    const int n_rows = p.N;  // weight rows per expert; gated tiles hold 64 + 64 of them
-    const int tiles = p.gated ? (n_rows / 2 + 63) / 64 : (n_rows + 127) / 128;
+    auto kern = int8_narrow_kernel<BT, GATED, BF16>;
+    if (!smem_ready(kern, C::SMEM, ready_dev)) return ST_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tiles * S, E, z);
+    cfg.gridDim = dim3(tiles * S, p.E, z);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
@@ -352,7 +586,43 @@ int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& 
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, int8_narrow_kernel<BT>, mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+}
+
+template <bool GATED, bool BF16>
+int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int num_sms,
+                cudaStream_t stream) {
+    static std::atomic<int> ready_dev{-1};
+    auto kern = int8_pair_kernel<GATED, BF16>;
+    if (!smem_ready(kern, Pair::SMEM, ready_dev)) return ST_CUDA;
+    kern<<<num_sms & ~1, Pair::THREADS, Pair::SMEM, stream>>>(mw, mx, p);
+    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+}
+
+template <bool GATED, bool BF16>
+int launch_t(const I8GemmArgs& g, const CUtensorMap& mw, const CUtensorMap& mx, cudaStream_t stream) {
+    const int nkb = (g.K + kKB - 1) / kKB;
+    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb,
+                     g.status, g.timeout_ns};
+    const int tiles = weight_tiles(g);
+    const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
+    if (per > 128) return launch_pair<GATED, BF16>(mw, mx, p, g.num_sms, stream);
+    // rows of one expert of a balanced routing, with three standard deviations
+    const int want = g.E == 1 ? g.R : std::min(g.R, per + static_cast<int>(3.0f * sqrtf(per)));
+    const int bt = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
+    const int z = g.E == 1 ? (g.R + bt - 1) / bt : 1;
+    // split K where the weight tiles leave SMs idle and an expert's rows are one block
+    int S = 1;
+    if (g.E == 1 || g.R <= bt) {
+        const long long units = static_cast<long long>(tiles) * z * std::min(g.E, g.R);
+        while (S < 8 && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
+    }
+    switch (bt) {
+        case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
+        case 32: return launch_narrow<32, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
+        case 64: return launch_narrow<64, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
+        default: return launch_narrow<128, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
+    }
 }
 
 }  // namespace
@@ -363,18 +633,9 @@ int launch_int8_gemm(const I8GemmArgs& g, cudaStream_t stream) {
     if (!make_map(&mw, g.b, static_cast<long long>(g.E) * g.N, g.K, kGran) ||
         !make_map(&mx, g.a, g.R, g.K, kGran))
         return ST_CUDA;
-    const int nkb = (g.K + kKB - 1) / kKB;
-    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, nkb, g.gated, g.out_bf16,
-                     g.status, g.timeout_ns};
-    const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
-    const int bt = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
-    const int z = std::min((per + bt - 1) / bt, 65535);
-    switch (bt) {
-        case 16: return launch_narrow<16>(mw, mx, p, g.E, 1, z, stream);
-        case 32: return launch_narrow<32>(mw, mx, p, g.E, 1, z, stream);
-        case 64: return launch_narrow<64>(mw, mx, p, g.E, 1, z, stream);
-        default: return launch_narrow<128>(mw, mx, p, g.E, 1, z, stream);
-    }
+    if (g.gated)
+        return g.out_bf16 ? launch_t<true, true>(g, mw, mx, stream) : launch_t<true, false>(g, mw, mx, stream);
+    return g.out_bf16 ? launch_t<false, true>(g, mw, mx, stream) : launch_t<false, false>(g, mw, mx, stream);
 }
 
 }  // namespace moe
