@@ -34,8 +34,8 @@ namespace {
 constexpr int kKB = 128;             // K bytes per stage
 constexpr int kWRows = 128;          // weight rows per CTA tile
 constexpr int kWBytes = kWRows * kKB;
-constexpr int kGran = 16;            // rows per TMA box
-constexpr int kBoxBytes = kGran * kKB;
+constexpr int kGran = 16;            // gate / up rows of a granule
+constexpr int kWBox = 64;            // weight rows per TMA box
 constexpr int kThreads = 192;        // warps: 0 TMA, 1 MMA, 2-5 epilogue
 constexpr int kEpiWarps = 4;
 
@@ -45,6 +45,7 @@ struct I8Params {
     const int32_t* m_indptr;
     void* out;
     int R, N, K, E, nkb;
+    int w_gran;   // gated with N / 2 not a multiple of 16: weight boxes of one half granule
     int* status;
     unsigned long long timeout_ns;
 };
@@ -111,15 +112,38 @@ template <int BT>
 struct Narrow {
     static constexpr int NST = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 3;
     static constexpr int STAGE = kWBytes + BT * kKB;
+    static constexpr int XBOX = BT < 32 ? BT : 32;   // token rows per TMA box
     static constexpr int COLS = 2 * BT < 32 ? 32 : 2 * BT;   // two accumulators
     static constexpr int SMEM = 1024 + NST * STAGE + 256;
 };
 
-// Global row of weight box i (16 rows) of 128-row tile wt of expert e.
+// Weight boxes of a stage: lane i < w_boxes loads box i of the 128-row tile wt
+// of expert e.  Plain: two boxes of 64 rows.  Gated: two boxes of two granules
+// (the map's dimensions are K, 16 rows, gate / up, granules, experts), or, when
+// granules would run over the end of a half, eight boxes of 16 rows.  Boxes of
+// 8 KB rather than 2 KB: with 2 KB boxes the copies' issue bounded the CTA-pair
+// kernel (K block of 128: ~1150 clocks against 512 of MMA).
 template <bool GATED>
-__device__ __forceinline__ int weight_box_row(const I8Params& p, int e, int wt, int i) {
-    if constexpr (!GATED) return e * p.N + wt * kWRows + i * kGran;
-    return e * p.N + ((i & 1) ? (p.N >> 1) : 0) + wt * (kWRows / 2) + (i >> 1) * kGran;
+__device__ __forceinline__ int w_boxes(const I8Params& p) {
+    return GATED && p.w_gran ? kWRows / kGran : kWRows / kWBox;
+}
+
+template <bool GATED, bool PAIR>
+__device__ __forceinline__ void load_weights(const I8Params& p, const CUtensorMap* map, uint8_t* stage,
+                                             uint64_t* bar, int kb, int e, int wt, int i) {
+    const int x = kb * kKB;
+    if (!GATED || p.w_gran) {
+        const int row = !GATED ? e * p.N + wt * kWRows + i * kWBox
+                               : e * p.N + ((i & 1) ? (p.N >> 1) : 0) + wt * (kWRows / 2) + (i >> 1) * kGran;
+        uint8_t* dst = stage + i * (GATED ? kGran : kWBox) * kKB;
+        if constexpr (PAIR) tma_load_2d_pair(dst, map, bar, x, row);
+        else tma_load_2d(dst, map, bar, x, row);
+    } else {
+        uint8_t* dst = stage + i * kWBox * kKB;
+        const int gran = (wt * (kWRows / kWBox) + i) * (kWBox / (2 * kGran));
+        if constexpr (PAIR) tma_load_5d_pair(dst, map, bar, x, 0, 0, gran, e);
+        else tma_load_5d(dst, map, bar, x, 0, 0, gran, e);
+    }
 }
 
 template <int BT, bool GATED, bool BF16>
@@ -174,23 +198,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kb1 = static_cast<int>(static_cast<long long>(p.nkb) * (ks + 1) / S);
 
     if (warp == 0) {
-        // lanes 0-7: the tile's eight 16-row weight boxes; lanes 8..: token boxes
-        const int wrow = weight_box_row<GATED>(p, e, wt, lane & 7);
+        // lanes 0..7: weight boxes, lanes 8..: token boxes
+        const int wb = w_boxes<GATED>(p);
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z) {
             const int row0 = lo + tb * BT;
-            const int boxes = (min(BT, hi - row0) + kGran - 1) / kGran;
+            const int boxes = (min(BT, hi - row0) + C::XBOX - 1) / C::XBOX;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
                 uint8_t* st = base + stage * C::STAGE;
-                if (lane == 0) mbar_arrive_expect_tx(&full[stage], (8 + boxes) * kBoxBytes);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[stage], kWBytes + boxes * C::XBOX * kKB);
                 __syncwarp();
-                if (lane < 8)
-                    tma_load_2d(st + lane * kBoxBytes, &tmW, &full[stage], kb * kKB, wrow);
-                else if (lane < 8 + boxes)
-                    tma_load_2d(st + lane * kBoxBytes, &tmX, &full[stage], kb * kKB,
-                                row0 + (lane - 8) * kGran);
+                if (lane < wb)
+                    load_weights<GATED, false>(p, &tmW, st, &full[stage], kb, e, wt, lane);
+                else if (lane >= 8 && lane < 8 + boxes)
+                    tma_load_2d(st + kWBytes + (lane - 8) * C::XBOX * kKB, &tmX, &full[stage], kb * kKB,
+                                row0 + (lane - 8) * C::XBOX);
                 __syncwarp();
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
@@ -310,6 +335,7 @@ struct Pair {
     static constexpr int NST = 6;
     static constexpr int BT = 256;
     static constexpr int STAGE = kWBytes + (BT / 2) * kKB;
+    static constexpr int XBOX = 64;                  // token rows per TMA box
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int MAX_E = 1024;
@@ -423,24 +449,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     };
 
     if (warp == 0) {
+        const int wb = w_boxes<GATED>(p);
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
             const Tile x = decode(t);
             const int half = ((x.rows + 31) & ~31) >> 1;      // token rows of this CTA
-            const int boxes = half / kGran;
-            const int wrow = weight_box_row<GATED>(p, x.e, x.wt, lane & 7);
-            const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * kGran;
+            const int boxes = (half + C::XBOX - 1) / C::XBOX;
+            const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * C::XBOX;
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
                 uint8_t* st = base + stage * C::STAGE;
                 if (rank == 0 && lane == 0)
-                    mbar_arrive_expect_tx(&full[stage], 2 * (8 + boxes) * kBoxBytes);
+                    mbar_arrive_expect_tx(&full[stage], 2 * (kWBytes + boxes * C::XBOX * kKB));
                 __syncwarp();
-                if (lane < 8)
-                    tma_load_2d_pair(st + lane * kBoxBytes, &tmW, &full[stage], kb * kKB, wrow);
-                else if (lane < 8 + boxes)
-                    tma_load_2d_pair(st + lane * kBoxBytes, &tmX, &full[stage], kb * kKB, xrow);
+                if (lane < wb)
+                    load_weights<GATED, true>(p, &tmW, st, &full[stage], kb, x.e, x.wt, lane);
+                else if (lane >= 8 && lane < 8 + boxes)
+                    tma_load_2d_pair(st + kWBytes + (lane - 8) * C::XBOX * kKB, &tmX, &full[stage],
+                                     kb * kKB, xrow);
                 __syncwarp();
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
@@ -536,18 +563,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// 2-D map of a row-major int8 matrix [rows, cols] with 16-row x 128-byte boxes
-// and the 128-byte swizzle; bytes past either end read 0.
-bool make_map(CUtensorMap* m, const void* ptr, long long rows, int cols, int box_rows) {
+bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
     auto fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(kKB), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t es[2] = {1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), dims, strides, box, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map of a row-major int8 matrix [rows, cols] with boxes of box_rows x 128
+// bytes and the 128-byte swizzle; bytes past either end read 0.
+bool make_map(CUtensorMap* m, const void* ptr, long long rows, int cols, int box_rows) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(kKB), static_cast<cuuint32_t>(box_rows)};
+    return encode(m, ptr, 2, dims, strides, box);
+}
+
+// Map of gated weights [E, 2, N/2, K] whose boxes are two granules: 16 gate
+// rows, their 16 up rows, twice.
+bool make_gated_map(CUtensorMap* m, const void* ptr, int E, int N, int K) {
+    const cuuint64_t k = K, half = N / 2;
+    const cuuint64_t dims[5] = {k, kGran, 2, half / kGran, static_cast<cuuint64_t>(E)};
+    const cuuint64_t strides[4] = {k, half * k, kGran * k, 2 * half * k};
+    const cuuint32_t box[5] = {kKB, kGran, 2, kWBox / (2 * kGran), 1};
+    return encode(m, ptr, 5, dims, strides, box);
 }
 
 // Opt-in of a kernel to its dynamic shared memory, once per device and kernel
@@ -600,13 +641,21 @@ int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p,
 }
 
 template <bool GATED, bool BF16>
-int launch_t(const I8GemmArgs& g, const CUtensorMap& mw, const CUtensorMap& mx, cudaStream_t stream) {
+int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int nkb = (g.K + kKB - 1) / kKB;
-    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb,
+    const int w_gran = GATED && (g.N / 2) % kGran ? 1 : 0;
+    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, w_gran,
                      g.status, g.timeout_ns};
+    CUtensorMap mw, mx;
+    if (GATED && !w_gran ? !make_gated_map(&mw, g.b, g.E, g.N, g.K)
+                         : !make_map(&mw, g.b, static_cast<long long>(g.E) * g.N, g.K, GATED ? kGran : kWBox))
+        return ST_CUDA;
     const int tiles = weight_tiles(g);
     const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
-    if (per > 128) return launch_pair<GATED, BF16>(mw, mx, p, g.num_sms, stream);
+    if (per > 128) {
+        if (!make_map(&mx, g.a, g.R, g.K, Pair::XBOX)) return ST_CUDA;
+        return launch_pair<GATED, BF16>(mw, mx, p, g.num_sms, stream);
+    }
     // rows of one expert of a balanced routing, with three standard deviations
     const int want = g.E == 1 ? g.R : std::min(g.R, per + static_cast<int>(3.0f * sqrtf(per)));
     const int bt = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
@@ -617,6 +666,7 @@ int launch_t(const I8GemmArgs& g, const CUtensorMap& mw, const CUtensorMap& mx, 
         const long long units = static_cast<long long>(tiles) * z * std::min(g.E, g.R);
         while (S < 8 && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
     }
+    if (!make_map(&mx, g.a, g.R, g.K, bt < 32 ? bt : 32)) return ST_CUDA;
     switch (bt) {
         case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
         case 32: return launch_narrow<32, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
@@ -629,13 +679,8 @@ int launch_t(const I8GemmArgs& g, const CUtensorMap& mw, const CUtensorMap& mx, 
 
 int launch_int8_gemm(const I8GemmArgs& g, cudaStream_t stream) {
     if (g.R == 0) return ST_OK;
-    CUtensorMap mw, mx;
-    if (!make_map(&mw, g.b, static_cast<long long>(g.E) * g.N, g.K, kGran) ||
-        !make_map(&mx, g.a, g.R, g.K, kGran))
-        return ST_CUDA;
-    if (g.gated)
-        return g.out_bf16 ? launch_t<true, true>(g, mw, mx, stream) : launch_t<true, false>(g, mw, mx, stream);
-    return g.out_bf16 ? launch_t<false, true>(g, mw, mx, stream) : launch_t<false, false>(g, mw, mx, stream);
+    if (g.gated) return g.out_bf16 ? launch_t<true, true>(g, stream) : launch_t<true, false>(g, stream);
+    return g.out_bf16 ? launch_t<false, true>(g, stream) : launch_t<false, false>(g, stream);
 }
 
 }  // namespace moe
