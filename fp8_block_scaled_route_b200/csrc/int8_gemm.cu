@@ -65,41 +65,122 @@ __device__ __forceinline__ void store_out(const I8Params& p, long long at, float
     if constexpr (BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
     else static_cast<float*>(p.out)[at] = v;
 }
+// Two neighbouring outputs, `at` even.
+template <bool BF16>
+__device__ __forceinline__ void store_out2(const I8Params& p, long long at, float a, float b) {
+    if constexpr (BF16)
+        reinterpret_cast<__nv_bfloat162*>(p.out)[at >> 1] = __floats2bfloat162_rn(a, b);
+    else
+        reinterpret_cast<float2*>(p.out)[at >> 1] = make_float2(a, b);
+}
 
-// Output of NC token columns: s[j] is the integer sum of token row row0 + j
-// and this lane's weight row (lane position `pos` of the 128-row tile).  Rows
-// at or past hi are not stored.  Called by whole warps.
-template <bool GATED, bool BF16, int NC>
-__device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], int e, int wt, int pos,
-                                     int row0, int hi) {
-    const int lane = threadIdx.x & 31;
-    const float as_l = lane < NC && row0 + lane < hi ? p.a_scale[row0 + lane] : 0.0f;
+// What a lane of the epilogue keeps for one weight tile: its weight row's
+// output column and scale.
+struct LaneCol {
+    int col;      // output column (gated: channel)
+    float scale;  // b_scale of the lane's weight row, 0 past the end
+    bool ok;
+};
+
+template <bool GATED>
+__device__ __forceinline__ LaneCol lane_col(const I8Params& p, int e, int wt, int pos) {
+    LaneCol c;
+    const float* bs = p.b_scale + static_cast<long long>(e) * p.N;
     if constexpr (!GATED) {
-        const int n = wt * kWRows + pos;
-        const bool ok = n < p.N;
-        const float bs = ok ? p.b_scale[static_cast<long long>(e) * p.N + n] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < NC; ++j) {
-            const float as = __shfl_sync(0xffffffffu, as_l, j);
-            if (ok && row0 + j < hi)
-                store_out<BF16>(p, static_cast<long long>(row0 + j) * p.N + n,
-                          __int2float_rn(s[j]) * as * bs);
-        }
+        c.col = wt * kWRows + pos;
+        c.ok = c.col < p.N;
+        c.scale = c.ok ? bs[c.col] : 0.0f;
     } else {
         const int half = p.N >> 1;
-        const int ch = wt * (kWRows / 2) + (pos >> 5) * kGran + (pos & 15);
-        const bool up = (lane & 16) != 0;
-        const bool ok = ch < half;
-        const float bs = ok ? p.b_scale[static_cast<long long>(e) * p.N + (up ? half : 0) + ch] : 0.0f;
+        c.col = wt * (kWRows / 2) + (pos >> 5) * kGran + (pos & 15);
+        c.ok = c.col < half;
+        c.scale = c.ok ? bs[((pos & 16) ? half : 0) + c.col] : 0.0f;
+    }
+    return c;
+}
+
+// A warp copies the scales of n <= 128 token rows from row0 on into its own
+// shared-memory buffer; rows at or past hi count as 0.
+__device__ __forceinline__ void stage_row_scales(const I8Params& p, float* as, int row0, int n, int hi) {
+    __syncwarp();
+    for (int i = threadIdx.x & 31; i < n; i += 32) as[i] = row0 + i < hi ? p.a_scale[row0 + i] : 0.0f;
+    __syncwarp();
+}
+
+// Output of NC token columns: s[j] is the integer sum of token row row0 + j
+// and this lane's weight row; as[j] is that token row's scale (shared memory,
+// 8-byte aligned).  Rows at or past hi are not stored.  Called by whole warps.
+//
+// Neighbouring lanes swap half of their results so that each stores two
+// neighbouring outputs of one row: half as many stores, and two columns' scale
+// products go through one packed multiply.  (One store per output, with the
+// row scales fetched by shuffles, took ~20 instructions an output and bounded
+// tiles of K = 2048: 8192 x 7168 x 2048 ran 105-130 us against 77 us for the
+// main loop alone.)
+template <bool GATED, bool BF16, int NC>
+__device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], const LaneCol& lc,
+                                     const float* as, int row0, int hi) {
+    const int lane = threadIdx.x & 31;
+    const int n_out = GATED ? p.N >> 1 : p.N;
+    const float2 bs = make_float2(lc.scale, lc.scale);
+    // G of token rows row0 + j and row0 + j + 1
+    auto two = [&](int j) {
+        const float2 f = make_float2(__int2float_rn(s[j]), __int2float_rn(s[j + 1]));
+        return __fmul2_rn(__fmul2_rn(f, *reinterpret_cast<const float2*>(as + j)), bs);
+    };
+    const bool odd = lane & 1;
+    const bool wide = (n_out & 1) == 0;
+    if constexpr (!GATED) {
+        if (wide) {
+            const long long at = static_cast<long long>(row0 + (odd ? 1 : 0)) * p.N + (lc.col & ~1);
+            const int lim = lc.ok ? hi - row0 - (odd ? 1 : 0) : 0;
 #pragma unroll
-        for (int j = 0; j < NC; j += 2) {
-            // the gate lane finishes token j, the up lane token j + 1
-            const float f0 = __int2float_rn(s[j]) * __shfl_sync(0xffffffffu, as_l, j) * bs;
-            const float f1 = __int2float_rn(s[j + 1]) * __shfl_sync(0xffffffffu, as_l, j + 1) * bs;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? f0 : f1, 16);
-            const float g = up ? got : f0, u = up ? f1 : got;
-            const int row = row0 + j + (up ? 1 : 0);
-            if (ok && row < hi) store_out<BF16>(p, static_cast<long long>(row) * half + ch, silu_fast(g) * u);
+            for (int j = 0; j < NC; j += 2) {
+                // the even lane finishes row j, the odd lane row j + 1
+                const float2 f = two(j);
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 1);
+                if (j < lim)
+                    store_out2<BF16>(p, at + static_cast<long long>(j) * p.N, odd ? got : f.x,
+                                     odd ? f.y : got);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; j += 2) {
+                const float2 f = two(j);
+                const long long at = static_cast<long long>(row0 + j) * p.N + lc.col;
+                if (lc.ok && row0 + j < hi) store_out<BF16>(p, at, f.x);
+                if (lc.ok && row0 + j + 1 < hi) store_out<BF16>(p, at + p.N, f.y);
+            }
+        }
+    } else {
+        const bool up = lane & 16;
+        // the gate lane gets the output of row j, the up lane that of row j + 1
+        auto gate_up = [&](int j) {
+            const float2 f = two(j);
+            const float got = __shfl_xor_sync(0xffffffffu, up ? f.x : f.y, 16);
+            return silu_fast(up ? got : f.x) * (up ? f.y : got);
+        };
+        const int first = up ? 1 : 0;
+        if (NC >= 4 && wide) {
+            const int mine = first + (odd ? 2 : 0);
+            const long long at = static_cast<long long>(row0 + mine) * n_out + (lc.col & ~1);
+            const int lim = lc.ok ? hi - row0 - mine : 0;
+#pragma unroll
+            for (int j = 0; j + 3 < NC; j += 4) {
+                const float v0 = gate_up(j), v1 = gate_up(j + 2);
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                if (j < lim)
+                    store_out2<BF16>(p, at + static_cast<long long>(j) * n_out, odd ? got : v0,
+                                     odd ? v1 : got);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NC; j += 2) {
+                const float v = gate_up(j);
+                const int row = row0 + j + first;
+                if (lc.ok && row < hi)
+                    store_out<BF16>(p, static_cast<long long>(row) * n_out + lc.col, v);
+            }
         }
     }
 }
@@ -114,7 +195,8 @@ struct Narrow {
     static constexpr int STAGE = kWBytes + BT * kKB;
     static constexpr int XBOX = BT < 32 ? BT : 32;   // token rows per TMA box
     static constexpr int COLS = 2 * BT < 32 ? 32 : 2 * BT;   // two accumulators
-    static constexpr int SMEM = 1024 + NST * STAGE + 256;
+    static constexpr int AS = kEpiWarps * BT * 4;    // row scales, a copy per epilogue warp
+    static constexpr int SMEM = 1024 + NST * STAGE + AS + 256;
 };
 
 // Weight boxes of a stage: lane i < w_boxes loads box i of the 128-row tile wt
@@ -162,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE);
+    float* as_all = reinterpret_cast<float*>(base + C::NST * C::STAGE);
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE + C::AS);
     uint64_t* empty = full + C::NST;
     uint64_t* tfull = empty + C::NST;    // [2]
     uint64_t* tempty = tfull + 2;        // [2]
@@ -258,10 +341,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int q = warp & 3;
         const int pos = q * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        float* as = as_all + q * BT;
+        const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
         uint32_t it = 0;
         for (int tb = blockIdx.z; tb < blocks; tb += gridDim.z, ++it) {
             const int row0 = lo + tb * BT;
             const int nt = (min(BT, hi - row0) + 15) & ~15;
+            stage_row_scales(p, as, row0, nt, hi);
             if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
             tc_fence_after();
             const uint32_t acc = lane_addr + (it & 1) * BT;
@@ -278,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     int s[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[j] = static_cast<int>(v[j]);
-                    emit<GATED, BF16, 16>(p, s, e, wt, pos, row0 + c, hi);
+                    emit<GATED, BF16, 16>(p, s, lc, as + c, row0 + c, hi);
                 }
             } else {
                 // one block per CTA: its partial sums go to shared memory, column by
@@ -304,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int row0 = lo + static_cast<int>(blockIdx.z) * BT;
             const int nt = min(BT, hi - row0);
             const uint32_t mine = smem_u32(base) + pos * 4;
+            const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
+            const float* as = as_all + (warp & 3) * BT;
             for (int c = 2 * ks; c < nt; c += 2 * S) {
                 int s[2] = {0, 0};
                 for (int r = 0; r < S; ++r) {
@@ -311,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     s[0] += ld_shared_cluster_s32(at + c * kWRows * 4);
                     s[1] += ld_shared_cluster_s32(at + (c + 1) * kWRows * 4);
                 }
-                emit<GATED, BF16, 2>(p, s, e, wt, pos, row0 + c, hi);
+                emit<GATED, BF16, 2>(p, s, lc, as + c, row0 + c, hi);
             }
         }
         __syncwarp();
@@ -340,17 +428,10 @@ struct Pair {
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int MAX_E = 1024;
     static constexpr int TABLE = ((MAX_E + 1) * 4 + 15) / 16 * 16;
-    static constexpr int SMEM = 1024 + NST * STAGE + TABLE + 256;
+    static constexpr int AS = EPI_WARPS * 128 * 4;   // row scales, 128 per epilogue warp
+    static constexpr int SMEM = 1024 + NST * STAGE + AS + TABLE + 256;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
-
-// A wait that also orders the waiting thread after cluster-scope arrivals.
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, const WaitCtl& wc,
-                                                  int where) {
-    const bool ok = warp_wait_spin(bar, parity, wc, where);
-    fence_acq_cluster();
-    return ok;
-}
 
 template <bool GATED, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
@@ -360,8 +441,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    int* tstart = reinterpret_cast<int*>(base + C::NST * C::STAGE);   // [E + 1] first tile
-    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE + C::TABLE);
+    float* as_all = reinterpret_cast<float*>(base + C::NST * C::STAGE);
+    int* tstart = reinterpret_cast<int*>(base + C::NST * C::STAGE + C::AS);   // [E + 1] first tile
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE + C::AS + C::TABLE);
     uint64_t* empty = full + C::NST;
     uint64_t* tfull = empty + C::NST;    // [2]
     uint64_t* tempty = tfull + 2;        // [2], the even CTA's
@@ -492,7 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 const Tile x = decode(t);
                 const uint32_t idesc = idesc_s8_s32(2 * kWRows, (x.rows + 31) & ~31);
                 const uint32_t acc = tmem + (it & 1) * C::BT;
-                if (!warp_wait_cluster(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
+                if (!warp_wait_spin(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
                 tc_fence_after();
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     if (!warp_wait_spin(&full[stage], phase, wc, 4)) { ok = false; break; }
@@ -521,25 +603,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         const int pos = q * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        float* as = as_all + (warp - 2) * 128;
         uint32_t it = 0;
         for (int t = blockIdx.x >> 1; t < total; t += stride, ++it) {
             const Tile x = decode(t);
             const int hi = x.row0 + x.rows;
+            const int c0 = part * 128, end = min(x.rows, c0 + 128);
+            const LaneCol lc = lane_col<GATED>(p, x.e, x.wt, pos);
+            stage_row_scales(p, as, x.row0 + c0, 128, hi);
             if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
             tc_fence_after();
             const uint32_t acc = lane_addr + (it & 1) * C::BT;
-            for (int c = part * 128; c < min(x.rows, part * 128 + 128); c += 32) {
+            for (int c = c0; c < end; c += 32) {
                 uint32_t v[32];
                 tmem_ld32_async(acc + c, v);
                 tmem_wait_ld(v);
+                if (c + 32 >= end) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(tempty0 + (it & 1) * 8);
+                }
                 int s[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) s[j] = static_cast<int>(v[j]);
-                emit<GATED, BF16, 32>(p, s, x.e, x.wt, pos, x.row0 + c, hi);
+                emit<GATED, BF16, 32>(p, s, lc, as + (c - c0), x.row0 + c, hi);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty0 + (it & 1) * 8);
+            if (end <= c0 && lane == 0) mbar_arrive_cluster(tempty0 + (it & 1) * 8);
         }
     }
     tc_fence_before();

@@ -439,13 +439,11 @@ __device__ __forceinline__ void umma_commit_pair_local(uint64_t* bar) {
             smem_u32(bar))
         : "memory");
 }
-// Arrives on a barrier of any CTA of the cluster, at cluster scope.
+// Arrives on a barrier of any CTA of the cluster.  Orders nothing but what the
+// caller's tcgen05 fences order (tensor-memory reads): a cluster-scope release
+// would wait for the warp's global stores.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-                 : "memory");
-}
-__device__ __forceinline__ void fence_acq_cluster() {
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t addr) {
