@@ -36,8 +36,6 @@ constexpr int kWRows = 128;          // weight rows per CTA tile
 constexpr int kWBytes = kWRows * kKB;
 constexpr int kGran = 16;            // gate / up rows of a granule
 constexpr int kWBox = 64;            // weight rows per TMA box
-constexpr int kThreads = 192;        // warps: 0 TMA, 1 MMA, 2-5 epilogue
-constexpr int kEpiWarps = 4;
 
 struct I8Params {
     const float* a_scale;
@@ -72,6 +70,21 @@ __device__ __forceinline__ void store_out2(const I8Params& p, long long at, floa
         reinterpret_cast<__nv_bfloat162*>(p.out)[at >> 1] = __floats2bfloat162_rn(a, b);
     else
         reinterpret_cast<float2*>(p.out)[at >> 1] = make_float2(a, b);
+}
+
+// A lane's NW output pairs of rows `rows` apart: pair i at element `at` + i *
+// pitch, stored while its row i * rows is below lim.
+template <bool BF16, int NW>
+__device__ __forceinline__ void store_rows(const I8Params& p, const float2 (&v)[NW], long long at,
+                                           long long pitch, int rows, int lim) {
+    if (lim >= rows * (NW - 1) + 1) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) store_out2<BF16>(p, at + i * pitch, v[i].x, v[i].y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            if (i * rows < lim) store_out2<BF16>(p, at + i * pitch, v[i].x, v[i].y);
+    }
 }
 
 // What a lane of the epilogue keeps for one weight tile: its weight row's
@@ -130,19 +143,21 @@ __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], cons
     };
     const bool odd = lane & 1;
     const bool wide = (n_out & 1) == 0;
+    // all results first, then the stores: their predicates would otherwise fence
+    // the chains of conversions, products and shuffles off from each other
+    constexpr int NW = NC / 2 / (GATED ? 2 : 1);   // pair stores of a lane
     if constexpr (!GATED) {
         if (wide) {
-            const long long at = static_cast<long long>(row0 + (odd ? 1 : 0)) * p.N + (lc.col & ~1);
-            const int lim = lc.ok ? hi - row0 - (odd ? 1 : 0) : 0;
+            // the even lane finishes rows j, the odd lane rows j + 1
+            float2 v[NW];
 #pragma unroll
-            for (int j = 0; j < NC; j += 2) {
-                // the even lane finishes row j, the odd lane row j + 1
-                const float2 f = two(j);
+            for (int i = 0; i < NW; ++i) {
+                const float2 f = two(2 * i);
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? f.x : f.y, 1);
-                if (j < lim)
-                    store_out2<BF16>(p, at + static_cast<long long>(j) * p.N, odd ? got : f.x,
-                                     odd ? f.y : got);
+                v[i] = make_float2(odd ? got : f.x, odd ? f.y : got);
             }
+            store_rows<BF16>(p, v, static_cast<long long>(row0 + (odd ? 1 : 0)) * p.N + (lc.col & ~1),
+                             2ll * p.N, 2, lc.ok ? hi - row0 - (odd ? 1 : 0) : 0);
         } else {
 #pragma unroll
             for (int j = 0; j < NC; j += 2) {
@@ -161,18 +176,17 @@ __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], cons
             return silu_fast(up ? got : f.x) * (up ? f.y : got);
         };
         const int first = up ? 1 : 0;
-        if (NC >= 4 && wide) {
+        if (NW > 0 && wide) {
             const int mine = first + (odd ? 2 : 0);
-            const long long at = static_cast<long long>(row0 + mine) * n_out + (lc.col & ~1);
-            const int lim = lc.ok ? hi - row0 - mine : 0;
+            float2 v[NW > 0 ? NW : 1];
 #pragma unroll
-            for (int j = 0; j + 3 < NC; j += 4) {
-                const float v0 = gate_up(j), v1 = gate_up(j + 2);
+            for (int i = 0; i < NW; ++i) {
+                const float v0 = gate_up(4 * i), v1 = gate_up(4 * i + 2);
                 const float got = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
-                if (j < lim)
-                    store_out2<BF16>(p, at + static_cast<long long>(j) * n_out, odd ? got : v0,
-                                     odd ? v1 : got);
+                v[i] = make_float2(odd ? got : v0, odd ? v1 : got);
             }
+            store_rows<BF16>(p, v, static_cast<long long>(row0 + mine) * n_out + (lc.col & ~1),
+                             4ll * n_out, 4, lc.ok ? hi - row0 - mine : 0);
         } else {
 #pragma unroll
             for (int j = 0; j < NC; j += 2) {
@@ -195,7 +209,12 @@ struct Narrow {
     static constexpr int STAGE = kWBytes + BT * kKB;
     static constexpr int XBOX = BT < 32 ? BT : 32;   // token rows per TMA box
     static constexpr int COLS = 2 * BT < 32 ? 32 : 2 * BT;   // two accumulators
-    static constexpr int AS = kEpiWarps * BT * 4;    // row scales, a copy per epilogue warp
+    // warps: 0 TMA, 1 MMA, then 4 epilogue warps, or 8 that share the columns
+    static constexpr int PARTS = BT >= 32 ? 2 : 1;
+    static constexpr int EPI_WARPS = 4 * PARTS;
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+    static constexpr int PCOLS = BT / PARTS;         // columns of a warp
+    static constexpr int AS = EPI_WARPS * PCOLS * 4; // row scales, PCOLS per epilogue warp
     static constexpr int SMEM = 1024 + NST * STAGE + AS + 256;
 };
 
@@ -229,7 +248,7 @@ __device__ __forceinline__ void load_weights(const I8Params& p, const CUtensorMa
 }
 
 template <int BT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
     int8_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const I8Params p, const int S) {
     using C = Narrow<BT>;
@@ -260,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], kEpiWarps);
+            mbar_init(&tempty[i], C::EPI_WARPS);
         }
         mbar_init(drain, 1);
         *abort_s = 0;
@@ -341,31 +360,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int q = warp & 3;
         const int pos = q * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        float* as = as_all + q * BT;
+        const int c0 = (warp - 2) / 4 * C::PCOLS;    // this warp's columns of a block
+        float* as = as_all + (warp - 2) * C::PCOLS;
         const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
         uint32_t it = 0;
         for (int tb = blockIdx.z; tb < blocks; tb += gridDim.z, ++it) {
-            const int row0 = lo + tb * BT;
-            const int nt = (min(BT, hi - row0) + 15) & ~15;
-            stage_row_scales(p, as, row0, nt, hi);
+            const int row0 = lo + tb * BT + c0;
+            const int nt = min(C::PCOLS, hi - row0);     // may be none
+            stage_row_scales(p, as, row0, C::PCOLS, hi);
             if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
             tc_fence_after();
-            const uint32_t acc = lane_addr + (it & 1) * BT;
+            const uint32_t acc = lane_addr + (it & 1) * BT + c0;
             if (S == 1) {
                 for (int c = 0; c < nt; c += 16) {
                     uint32_t v[16];
                     tmem_ld16_async(acc + c, v);
                     tmem_wait_ld(v);
-                    if (c + 16 >= nt) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[it & 1]);
-                    }
                     int s[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) s[j] = static_cast<int>(v[j]);
                     emit<GATED, BF16, 16>(p, s, lc, as + c, row0 + c, hi);
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[it & 1]);
             } else {
                 // one block per CTA: its partial sums go to shared memory, column by
                 // column (the pipeline's stages are free: every MMA has completed)
@@ -375,14 +393,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                     tmem_ld16_async(acc + c, v);
                     tmem_wait_ld(v);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * kWRows + pos] = static_cast<int>(v[j]);
+                    for (int j = 0; j < 16; ++j) part[(c0 + c + j) * kWRows + pos] = static_cast<int>(v[j]);
                 }
             }
         }
     }
     if (S > 1) {
-        // every thread of the cluster: partial sums visible, then pair columns
-        // (2i, 2i + 1) are added up and written by CTA i mod S
+        // every thread of the cluster: partial sums visible; then the pair
+        // columns (2 i, 2 i + 1) are added up and written, i mod S by CTA, then
+        // in turn by the CTA's groups of four epilogue warps
         __syncwarp();
         cluster_sync_all();
         if (warp >= 2 && !*abort_s) {
@@ -391,15 +410,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int nt = min(BT, hi - row0);
             const uint32_t mine = smem_u32(base) + pos * 4;
             const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
-            const float* as = as_all + (warp & 3) * BT;
-            for (int c = 2 * ks; c < nt; c += 2 * S) {
+            for (int c = 2 * (ks + S * ((warp - 2) / 4)); c < nt; c += 2 * S * C::PARTS) {
                 int s[2] = {0, 0};
                 for (int r = 0; r < S; ++r) {
                     const uint32_t at = mapa_shared(mine, r);
                     s[0] += ld_shared_cluster_s32(at + c * kWRows * 4);
                     s[1] += ld_shared_cluster_s32(at + (c + 1) * kWRows * 4);
                 }
-                emit<GATED, BF16, 2>(p, s, lc, as + c, row0 + c, hi);
+                // column c's scales are in the buffer of the warp of its part and lanes
+                const float* as = as_all + ((c / C::PCOLS) * 4 + ((warp - 2) & 3)) * C::PCOLS + c % C::PCOLS;
+                emit<GATED, BF16, 2>(p, s, lc, as, row0 + c, hi);
             }
         }
         __syncwarp();
@@ -706,7 +726,7 @@ int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& 
     if (!smem_ready(kern, C::SMEM, ready_dev)) return ST_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(tiles * S, p.E, z);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
