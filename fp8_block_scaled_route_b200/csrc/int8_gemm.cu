@@ -36,6 +36,7 @@ constexpr int kWRows = 128;          // weight rows per CTA tile
 constexpr int kWBytes = kWRows * kKB;
 constexpr int kGran = 16;            // gate / up rows of a granule
 constexpr int kWBox = 64;            // weight rows per TMA box
+constexpr int kMaxSplit = 8;         // CTAs of a cluster that share a K range
 
 struct I8Params {
     const float* a_scale;
@@ -43,6 +44,8 @@ struct I8Params {
     const int32_t* m_indptr;
     void* out;
     int R, N, K, E, nkb;
+    int bt;       // pair kernel: token rows of a tile (64, 128 or 256)
+    int nst;      // pair kernel: stages
     int w_gran;   // gated with N / 2 not a multiple of 16: weight boxes of one half granule
     int* status;
     unsigned long long timeout_ns;
@@ -411,11 +414,21 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
             const uint32_t mine = smem_u32(base) + pos * 4;
             const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
             for (int c = 2 * (ks + S * ((warp - 2) / 4)); c < nt; c += 2 * S * C::PARTS) {
+                int t[kMaxSplit][2];     // every load in flight before the sums
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r) {
+                    t[r][0] = t[r][1] = 0;
+                    if (r < S) {
+                        const uint32_t at = mapa_shared(mine, r) + c * kWRows * 4;
+                        t[r][0] = ld_shared_cluster_s32(at);
+                        t[r][1] = ld_shared_cluster_s32(at + kWRows * 4);
+                    }
+                }
                 int s[2] = {0, 0};
-                for (int r = 0; r < S; ++r) {
-                    const uint32_t at = mapa_shared(mine, r);
-                    s[0] += ld_shared_cluster_s32(at + c * kWRows * 4);
-                    s[1] += ld_shared_cluster_s32(at + (c + 1) * kWRows * 4);
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r) {
+                    s[0] += t[r][0];
+                    s[1] += t[r][1];
                 }
                 // column c's scales are in the buffer of the warp of its part and lanes
                 const float* as = as_all + ((c / C::PCOLS) * 4 + ((warp - 2) & 3)) * C::PCOLS + c % C::PCOLS;
@@ -439,18 +452,24 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
 // thirds of what a single-CTA 128 x 256 tile loads.  Two 256-column
 // accumulators in tensor memory let the epilogue of one tile run under the
 // next tile's main loop.
+// The ring holds as many stages as fit whatever the tile (6 of 32 KB to 9 of
+// 20 KB): a copy takes ~1.8 us under load, so the bytes in flight set the rate.
 struct Pair {
-    static constexpr int NST = 6;
-    static constexpr int BT = 256;
-    static constexpr int STAGE = kWBytes + (BT / 2) * kKB;
-    static constexpr int XBOX = 64;                  // token rows per TMA box
+    static constexpr int BT = 256;                   // largest tile; accumulators are this far apart
+    static constexpr int MAX_NST = 9;
+    static constexpr int RING = 6 * (kWBytes + BT / 2 * kKB);
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int MAX_E = 1024;
-    static constexpr int TABLE = ((MAX_E + 1) * 4 + 15) / 16 * 16;
     static constexpr int AS = EPI_WARPS * 128 * 4;   // row scales, 128 per epilogue warp
-    static constexpr int SMEM = 1024 + NST * STAGE + AS + TABLE + 256;
+    static constexpr int TABLE = ((MAX_E + 1) * 4 + 15) / 16 * 16;
+    static constexpr int SMEM = 1024 + RING + AS + TABLE + 256;
     static_assert(SMEM <= 232448, "shared memory budget");
+    static constexpr int stage_bytes(int bt) { return kWBytes + bt / 2 * kKB; }
+    static constexpr int stages(int bt) {
+        return RING / stage_bytes(bt) < MAX_NST ? RING / stage_bytes(bt) : MAX_NST;
+    }
+    static constexpr int xbox(int bt) { return bt / 2 < 64 ? bt / 2 : 64; }   // token rows per TMA box
 };
 
 template <bool GATED, bool BF16>
@@ -461,19 +480,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    float* as_all = reinterpret_cast<float*>(base + C::NST * C::STAGE);
-    int* tstart = reinterpret_cast<int*>(base + C::NST * C::STAGE + C::AS);   // [E + 1] first tile
-    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::NST * C::STAGE + C::AS + C::TABLE);
-    uint64_t* empty = full + C::NST;
-    uint64_t* tfull = empty + C::NST;    // [2]
+    float* as_all = reinterpret_cast<float*>(base + C::RING);
+    int* tstart = reinterpret_cast<int*>(base + C::RING + C::AS);   // [E + 1] first tile
+    uint64_t* full = reinterpret_cast<uint64_t*>(base + C::RING + C::AS + C::TABLE);
+    uint64_t* empty = full + C::MAX_NST;
+    uint64_t* tfull = empty + C::MAX_NST;    // [2]
     uint64_t* tempty = tfull + 2;        // [2], the even CTA's
     uint64_t* drain = tempty + 2;
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_s + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
+    const int nst = p.nst, stage_bytes = kWBytes + p.bt * (kKB / 2);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::NST; ++i) {
+        for (int i = 0; i < nst; ++i) {
             mbar_init(&full[i], 1);      // the even CTA's producer; both CTAs' bytes
             mbar_init(&empty[i], 1);
         }
@@ -502,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             int lo, hi;
             expert_rows(p, e, lo, hi);
             tstart[e] = hi - lo;         // rows, replaced below
-            sum += ((hi - lo + C::BT - 1) / C::BT) * wtiles;
+            sum += ((hi - lo + p.bt - 1) / p.bt) * wtiles;
         }
         int incl = sum;
 #pragma unroll
@@ -512,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         }
         int run = incl - sum;
         for (int e = e0; e < e1; ++e) {
-            const int n = (tstart[e] + C::BT - 1) / C::BT * wtiles;
+            const int n = (tstart[e] + p.bt - 1) / p.bt * wtiles;
             tstart[e] = run;
             run += n;
         }
@@ -540,40 +560,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         int r0, r1;
         expert_rows(p, lo, r0, r1);
         const int local = t - tstart[lo];
-        const int blocks = (r1 - r0 + C::BT - 1) / C::BT;
+        const int blocks = (r1 - r0 + p.bt - 1) / p.bt;
         const int w = local / blocks;
         Tile x;
         x.e = lo;
         x.wt = 2 * w + static_cast<int>(rank);
-        x.row0 = r0 + (local - w * blocks) * C::BT;
-        x.rows = min(C::BT, r1 - x.row0);
+        x.row0 = r0 + (local - w * blocks) * p.bt;
+        x.rows = min(p.bt, r1 - x.row0);
         return x;
     };
 
     if (warp == 0) {
         const int wb = w_boxes<GATED>(p);
+        const int xbox = min(p.bt >> 1, 64);          // token rows per box
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
             const Tile x = decode(t);
             const int half = ((x.rows + 31) & ~31) >> 1;      // token rows of this CTA
-            const int boxes = (half + C::XBOX - 1) / C::XBOX;
-            const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * C::XBOX;
+            const int boxes = (half + xbox - 1) / xbox;
+            const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * xbox;
             for (int kb = 0; kb < p.nkb; ++kb) {
                 if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
-                uint8_t* st = base + stage * C::STAGE;
+                uint8_t* st = base + stage * stage_bytes;
                 if (rank == 0 && lane == 0)
-                    mbar_arrive_expect_tx(&full[stage], 2 * (kWBytes + boxes * C::XBOX * kKB));
+                    mbar_arrive_expect_tx(&full[stage], 2 * (kWBytes + boxes * xbox * kKB));
                 __syncwarp();
                 if (lane < wb)
                     load_weights<GATED, true>(p, &tmW, st, &full[stage], kb, x.e, x.wt, lane);
                 else if (lane >= 8 && lane < 8 + boxes)
-                    tma_load_2d_pair(st + kWBytes + (lane - 8) * C::XBOX * kKB, &tmX, &full[stage],
+                    tma_load_2d_pair(st + kWBytes + (lane - 8) * xbox * kKB, &tmX, &full[stage],
                                      kb * kKB, xrow);
                 __syncwarp();
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
-                if (++stage == C::NST) { stage = 0; phase ^= 1; }
+                if (++stage == nst) { stage = 0; phase ^= 1; }
             }
         }
         // No copy and no arrival may still be on its way when the CTA ends.  The
@@ -581,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         // the MMAs have released its stages.  After an abort one wait runs out
         // (2 s, long after any copy has landed) and the rest are skipped.
         uint64_t* last = rank == 0 ? full : empty;
-        for (int st = 0; st < C::NST; ++st)
+        for (int st = 0; st < nst; ++st)
             if (((armed >> st) & 1u) &&
                 !wait_bar(&last[st], (armed_par >> st) & 1u, wc, 2, /*drain=*/true))
                 break;
@@ -599,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 for (int kb = 0; kb < p.nkb; ++kb) {
                     if (!warp_wait_spin(&full[stage], phase, wc, 4)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t sw = smem_u32(base + stage * C::STAGE);
+                    const uint32_t sw = smem_u32(base + stage * stage_bytes);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
@@ -609,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                         if (kb == p.nkb - 1) umma_commit_pair(&tfull[it & 1]);
                     }
                     __syncwarp();
-                    if (++stage == C::NST) { stage = 0; phase ^= 1; }
+                    if (++stage == nst) { stage = 0; phase ^= 1; }
                 }
             }
             if (elect_one()) umma_commit_pair_local(drain);
@@ -717,6 +738,28 @@ int weight_tiles(const I8GemmArgs& g) {
     return g.gated ? (g.N / 2 + 63) / 64 : (g.N + 127) / 128;
 }
 
+// Token rows of a pair tile: the fewest clocks for a balanced routing.  A
+// 128-byte K block costs an SM its loads, 16 KB of weights and 64 bytes a token
+// row at ~58 B/clk (measured), or 2 clocks of MMA a token row; a tile adds ~3000
+// clocks of pipeline fill and epilogue.  Smaller tiles pay where 256-row ones
+// leave pairs idle: 256 rows x 4096 x 7168: tiles of 256 rows 24.5 us, of 64
+// rows 21.8 us.
+int pair_tile(const I8GemmArgs& g, int per, int tiles) {
+    const long long pairs = g.num_sms / 2, nkb = (g.K + kKB - 1) / kKB;
+    const long long w = static_cast<long long>(std::min(g.E, g.R)) * ((tiles + 1) / 2);
+    int best = 256;
+    long long best_cost = 0;
+    for (int bt = 256; bt >= 64; bt /= 2) {
+        const long long waves = (w * ((per + bt - 1) / bt) + pairs - 1) / pairs;
+        const long long cost = waves * (nkb * std::max(2 * bt, (16384 + 64 * bt) / 58) + 3000);
+        if (best_cost == 0 || cost < best_cost) {
+            best = bt;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
 template <int BT, bool GATED, bool BF16>
 int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int tiles, int S,
                   int z, cudaStream_t stream) {
@@ -753,7 +796,7 @@ template <bool GATED, bool BF16>
 int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int nkb = (g.K + kKB - 1) / kKB;
     const int w_gran = GATED && (g.N / 2) % kGran ? 1 : 0;
-    const I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, w_gran,
+    I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, 0, 0, w_gran,
                      g.status, g.timeout_ns};
     CUtensorMap mw, mx;
     if (GATED && !w_gran ? !make_gated_map(&mw, g.b, g.E, g.N, g.K)
@@ -762,7 +805,9 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int tiles = weight_tiles(g);
     const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
     if (per > 128) {
-        if (!make_map(&mx, g.a, g.R, g.K, Pair::XBOX)) return ST_CUDA;
+        p.bt = pair_tile(g, per, tiles);
+        p.nst = Pair::stages(p.bt);
+        if (!make_map(&mx, g.a, g.R, g.K, Pair::xbox(p.bt))) return ST_CUDA;
         return launch_pair<GATED, BF16>(mw, mx, p, g.num_sms, stream);
     }
     // rows of one expert of a balanced routing, with three standard deviations
@@ -773,7 +818,7 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     int S = 1;
     if (g.E == 1 || g.R <= bt) {
         const long long units = static_cast<long long>(tiles) * z * std::min(g.E, g.R);
-        while (S < 8 && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
+        while (S < kMaxSplit && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
     }
     if (!make_map(&mx, g.a, g.R, g.K, bt < 32 ? bt : 32)) return ST_CUDA;
     switch (bt) {
