@@ -17,9 +17,6 @@
 //                    time; lanes with the same expert are ranked with
 //                    one warp ballot per expert-id bit, so each pair lands at
 //                    chunk_base[e] + (earlier pairs of e in the chunk).
-#include <cuda_bf16.h>
-
-#include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
@@ -481,429 +478,6 @@ int launch_route_permute(const RouteArgs& r, cudaStream_t stream) {
         if (cudaGetLastError() != cudaSuccess) return ST_CUDA;
     }
     return ST_OK;
-}
-
-// ------------------------------------------------------------ scored router
-// Expert choice by scores (launch_router_score).  For token t, with x the
-// logits and b the bias:
-//   p_e = 1 / (1 + exp(-x_e)) or softmax(x)_e;  c_e = p_e + b_e (the order of
-//   x without a bias);  group g = E / n_group consecutive experts, G_g = the
-//   sum of its group_top (1 or 2) largest c;  candidates: the topk_group
-//   groups with the largest G;  ids: the k largest c among them, descending,
-//   ties to the lower index;  w_j = p_j (/ sum p) * scale.
-// Masked experts (logit NaN or at most its type's lowest value, bias NaN or at
-// most -FLT_MAX) rank after every other, by index, and get weight 0.
-//
-// One warp per token, lane l holding experts l + 32 i.  The choice is that of
-// 64-bit values at 32-bit speed: c is computed in fp32, whose error is bounded
-// (score_tol), and only a token with two neighbouring values closer than the
-// bound (among its k winners, at the k / k + 1 border, or at the border
-// between chosen and dropped groups) is decided again with 64-bit scores.
-// Each winner costs one warp-wide integer maximum over order-preserving keys
-// of the values (a reduction instruction, where a shuffle tree of (value,
-// index) pairs takes ten shuffles and as many selects).
-
-constexpr float kFltMax = 3.402823466e38f;
-constexpr float kBf16Lowest = -3.38953138925153547590e38f;
-
-__device__ __forceinline__ float ld_logit(const float* l, int e) { return l[e]; }
-__device__ __forceinline__ float ld_logit(const __nv_bfloat16* l, int e) {
-    return __bfloat162float(l[e]);
-}
-__device__ __forceinline__ bool logit_masked(const float*, float x) { return !(x > -kFltMax); }
-__device__ __forceinline__ bool logit_masked(const __nv_bfloat16*, float x) {
-    return !(x > kBf16Lowest);
-}
-
-// Order-preserving map of finite floats to [0x00800000, 0xff7fffff]; 1 is a
-// masked expert, 0 no candidate.
-__device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);  // -0 and +0 compare equal
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
-
-// Bound on |difference of two fp32 selection values - the exact difference|.
-// Scores use the hardware exponential, whose relative error is (2 + 1.17 |z|)
-// ulp at argument z, and the correctly rounded reciprocal.
-//  sigmoid + b: p (1 - p) (2 + 1.17 |x|) + 2 ulps <= 3 * 2^-24 per score, plus
-//    one rounding of the sum; four scores in a difference of group sums: 2^-19
-//    and 2^-21 of the values' size.
-//  softmax + b: the 37-term sum's relative error 40 * 2^-24 times p, and sum
-//    p <= 1: 2^-17, the same relative part.
-//  no bias (group sums of scores alone): relative only; |z| <= 88 before the
-//    exponential leaves fp32's normal range: (2 + 2.2 * 88 + 40) 2^-24 < 2^-15.
-__device__ __forceinline__ float score_tol(const ScoreArgs& a, float v) {
-    const float m = fabsf(v);
-    if (!a.bias) return 3.0517578125e-05f * m;
-    return (a.sigmoid ? 1.9073486328125e-06f : 7.62939453125e-06f) + 4.76837158203125e-07f * m;
-}
-
-// The choice with 64-bit scores; lane j < k returns the j-th expert.
-template <int PER, typename LT>
-__device__ __noinline__ int score_choose_f64(const ScoreArgs& a, const LT* l) {
-    const int lane = threadIdx.x & 31;
-    const int gs = a.E / a.n_group;
-    const double none = -__longlong_as_double(0x7ff0000000000000ll);
-    double mx = none, z = 0.0;
-    if (!a.sigmoid) {
-        for (int i = 0; i < PER; ++i) {
-            const int e = lane + 32 * i;
-            if (e >= a.E) break;
-            const float x = ld_logit(l, e);
-            const bool m = logit_masked(l, x) || (a.bias && !(a.bias[e] > -kFltMax));
-            if (!m) mx = fmax(mx, static_cast<double>(fminf(x, kFltMax)));
-        }
-        for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        for (int i = 0; i < PER; ++i) {
-            const int e = lane + 32 * i;
-            if (e >= a.E) break;
-            const float x = ld_logit(l, e);
-            const bool m = logit_masked(l, x) || (a.bias && !(a.bias[e] > -kFltMax));
-            if (!m) z += exp(static_cast<double>(fminf(x, kFltMax)) - mx);
-        }
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    }
-    // c: value the experts are ordered by; p: value that group sums add up
-    double c[PER], p[PER];
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        c[i] = p[i] = none;
-        if (e >= a.E) continue;
-        float x = ld_logit(l, e);
-        if (logit_masked(l, x) || (a.bias && !(a.bias[e] > -kFltMax))) continue;
-        x = fminf(x, kFltMax);
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(x)))
-                                   : exp(static_cast<double>(x) - mx) / z;
-        c[i] = a.bias ? s + static_cast<double>(fminf(a.bias[e], kFltMax)) : static_cast<double>(x);
-        p[i] = a.bias || a.group_top == 1 ? c[i] : s;
-    }
-    uint32_t groups = 1u;
-    if (a.n_group > 1) {
-        double mine = none;  // lane g: group g's value
-        for (int g = 0; g < a.n_group; ++g) {
-            double t1 = none, t2 = none;
-            for (int i = 0; i < PER; ++i) {
-                const int e = lane + 32 * i;
-                if (e < g * gs || e >= (g + 1) * gs) continue;
-                t2 = fmax(t2, fmin(t1, p[i]));
-                t1 = fmax(t1, p[i]);
-            }
-            for (int o = 16; o > 0; o >>= 1) {
-                const double u1 = __shfl_xor_sync(0xffffffffu, t1, o);
-                const double u2 = __shfl_xor_sync(0xffffffffu, t2, o);
-                t2 = fmax(fmin(t1, u1), fmax(t2, u2));
-                t1 = fmax(t1, u1);
-            }
-            const double v = a.group_top == 2 && t2 != none ? t1 + t2 : t1;
-            if (lane == g) mine = v;
-        }
-        int rank = 0;
-        for (int g = 0; g < a.n_group; ++g) {
-            const double v = __shfl_sync(0xffffffffu, mine, g);
-            rank += v > mine || (v == mine && g < lane) ? 1 : 0;
-        }
-        groups = __ballot_sync(0xffffffffu, lane < a.n_group && rank < a.topk_group);
-    }
-    uint32_t gone = 0;
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        if (e >= a.E || !((groups >> (e / gs)) & 1u)) gone |= 1u << i;
-    }
-    int chosen = 0;
-    for (int j = 0; j < a.k; ++j) {
-        double bv = none;
-        int be = 0x7fffffff;  // none
-        for (int i = 0; i < PER; ++i) {
-            if ((gone >> i) & 1u) continue;
-            if (be == 0x7fffffff || c[i] > bv) {
-                bv = c[i];
-                be = lane + 32 * i;
-            }
-        }
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(0xffffffffu, bv, o);
-            const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-            if (oe != 0x7fffffff && (be == 0x7fffffff || ov > bv || (ov == bv && oe < be))) {
-                bv = ov;
-                be = oe;
-            }
-        }
-        if (lane == (be & 31)) gone |= 1u << (be >> 5);
-        if (lane == j) chosen = be;
-    }
-    return chosen;
-}
-
-// One token.  scratch: E floats of this warp's shared memory (groups only).
-template <int PER, typename LT>
-__device__ __forceinline__ void router_score_token(const ScoreArgs& a, int t, float* scratch) {
-    const int lane = threadIdx.x & 31;
-    const LT* l = static_cast<const LT*>(a.logits) + static_cast<long long>(t) * a.E;
-    const bool sums = a.n_group > 1 && a.group_top == 2;   // group values add scores up
-    const bool need_score = a.bias != nullptr || sums;
-    const bool need_z = !a.sigmoid && (need_score || !a.renorm);
-    float v[PER];                  // logits, then the selection values
-    uint32_t masked = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < a.E ? ld_logit(l, e) : -kFltMax;
-    }
-    uint32_t mkey = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        const bool m = e >= a.E || logit_masked(l, v[i]) || (a.bias && !(a.bias[e] > -kFltMax));
-        v[i] = fminf(v[i], kFltMax);
-        masked |= (m ? 1u : 0u) << i;
-        if (!m) mkey = max(mkey, order_key(v[i]));
-    }
-    float mx = 0.0f, zinv = 0.0f;
-    if (need_z) {
-        mkey = __reduce_max_sync(0xffffffffu, mkey);
-        mx = mkey ? key_value(mkey) : 0.0f;
-        float z = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (!((masked >> i) & 1u)) z += __expf(v[i] - mx);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        zinv = z > 0.0f ? __frcp_rn(z) : 0.0f;
-    }
-    const int gs = a.E / a.n_group;
-    bool ambiguous = false;
-    uint32_t groups = 1u;
-    if (need_score || a.n_group > 1) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.E) {
-                float g = v[i];
-                if (need_score) {
-                    const float s = a.sigmoid ? __frcp_rn(1.0f + __expf(-v[i]))
-                                              : __expf(v[i] - mx) * zinv;
-                    if (a.bias) v[i] = s + fminf(a.bias[e], kFltMax);
-                    g = a.bias || !sums ? v[i] : s;
-                }
-                if (a.n_group > 1) scratch[e] = (masked >> i) & 1u ? -INFINITY : g;
-            }
-        }
-    }
-    if (a.n_group > 1) {
-        // P lanes scan a group together (P * n_group <= 32), then merge
-        __syncwarp();
-        int lg = 0;
-        while ((1 << lg) < a.n_group) ++lg;
-        const int P = 32 >> lg;
-        const int g = lane >> (5 - lg), sub = lane & (P - 1);
-        float t1 = -INFINITY, t2 = -INFINITY;
-        if (g < a.n_group)
-            for (int i = sub; i < gs; i += P) {
-                const float f = scratch[g * gs + i];
-                t2 = fmaxf(t2, fminf(t1, f));
-                t1 = fmaxf(t1, f);
-            }
-        for (int o = P >> 1; o > 0; o >>= 1) {
-            const float u1 = __shfl_xor_sync(0xffffffffu, t1, o);
-            const float u2 = __shfl_xor_sync(0xffffffffu, t2, o);
-            t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
-            t1 = fmaxf(t1, u1);
-        }
-        float gv = a.group_top == 2 && t2 > -INFINITY ? t1 + t2 : t1;
-        gv = __shfl_sync(0xffffffffu, gv, (lane << (5 - lg)) & 31);  // lane g: group g's value
-        int rank = 0;
-        for (int o = 0; o < a.n_group; ++o) {
-            const float ov = __shfl_sync(0xffffffffu, gv, o);
-            rank += ov > gv || (ov == gv && o < lane) ? 1 : 0;
-        }
-        const bool in = lane < a.n_group && rank < a.topk_group;
-        groups = __ballot_sync(0xffffffffu, in);
-        if (need_score && a.topk_group < a.n_group) {
-            const bool live = lane < a.n_group && gv > -INFINITY;
-            const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(gv) : 0xffffffffu);
-            const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(gv) : 0u);
-            if (lo != 0xffffffffu && hi != 0u) {
-                const float fl = key_value(lo), fh = key_value(hi);
-                ambiguous = !(fl - fh > fmaxf(score_tol(a, fl), score_tol(a, fh)));
-            }
-        }
-        __syncwarp();
-    }
-    // keys of the candidates, and the lane's best
-    uint32_t key[PER];
-    const uint32_t inv_gs = ((1u << 20) + gs - 1) / gs;  // e / gs = e * inv_gs >> 20 for e, gs <= 1024
-    uint32_t bk = 0;
-    int be = 0x7fffffff;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        const bool cand = e < a.E && (a.n_group == 1 || ((groups >> ((e * inv_gs) >> 20)) & 1u));
-        key[i] = !cand ? 0u : (masked >> i) & 1u ? 1u : order_key(v[i]);
-        if (key[i] > bk) {
-            bk = key[i];
-            be = e;
-        }
-    }
-    // one winner more than wanted where the k / k + 1 border has to be checked
-    const int rounds = a.bias && a.k < a.topk_group * gs ? a.k + 1 : a.k;
-    int mine = 0;
-    uint32_t mine_key = 0, next_key = 0;  // next_key: of the winner after this lane's
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
-        const uint32_t who = __ballot_sync(0xffffffffu, bk == top);
-        const int e = (who & (who - 1)) == 0
-                          ? __shfl_sync(0xffffffffu, be, __ffs(who) - 1)
-                          : static_cast<int>(__reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff));
-        if (lane == j) {
-            mine = e;
-            mine_key = top;
-        }
-        if (lane == j - 1) next_key = top;
-        if (lane == (e & 31)) {
-            bk = 0;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (lane + 32 * i == e) key[i] = 0;
-                if (key[i] > bk) {
-                    bk = key[i];
-                    be = lane + 32 * i;
-                }
-            }
-        }
-    }
-    if (a.bias && !ambiguous) {
-        bool close = false;
-        if (lane < rounds - 1 && next_key > 1u) {
-            const float f0 = key_value(mine_key), f1 = key_value(next_key);
-            close = !(f0 - f1 > fmaxf(score_tol(a, f0), score_tol(a, f1)));
-        }
-        if (__any_sync(0xffffffffu, close)) {
-            // equal logits with equal biases tie exactly: their order is by index
-            // (not at the k / k + 1 border, behind which more may be close)
-            const int other = __shfl_down_sync(0xffffffffu, mine, 1);
-            if (close && lane + 1 < a.k)
-                close = !(ld_logit(l, mine) == ld_logit(l, other) && a.bias[mine] == a.bias[other]);
-            ambiguous = __any_sync(0xffffffffu, close);
-        }
-    }
-    if (ambiguous) mine = score_choose_f64<PER, LT>(a, l);
-    // weights of the k winners, lane j = slot j
-    const bool slot = lane < a.k;
-    float x = -kFltMax;
-    bool off = true;
-    if (slot) {
-        x = ld_logit(l, mine);
-        off = logit_masked(l, x) || (a.bias && !(a.bias[mine] > -kFltMax));
-        x = fminf(x, kFltMax);
-    }
-    float u = 0.0f;
-    if (a.renorm) {
-        // scaled by the largest so that no row of small scores underflows
-        const uint32_t xk = __reduce_max_sync(0xffffffffu, off ? 0u : order_key(x));
-        float m = xk ? key_value(xk) : 0.0f;
-        if (a.sigmoid) m = fminf(m, 0.0f);
-        if (!off)
-            u = !a.sigmoid ? expf(x - m) : x > 0.0f ? 1.0f / (1.0f + expf(-x))
-                                                    : expf(x - m) / (1.0f + expf(x));
-        float sum = u;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        u = sum > 0.0f ? __fdiv_rn(u, sum) : 0.0f;
-    } else if (!off) {
-        u = !a.sigmoid ? expf(x - mx) * zinv : x > 0.0f ? 1.0f / (1.0f + expf(-x))
-                                                        : expf(x) / (1.0f + expf(x));
-    }
-    if (slot) {
-        a.ids[static_cast<long long>(t) * a.k + lane] = mine;
-        a.w[static_cast<long long>(t) * a.k + lane] = u * a.scale;
-    }
-}
-
-template <int PER, typename LT>
-__global__ void __launch_bounds__(128) router_score_kernel(const ScoreArgs a) {
-    extern __shared__ float group_scratch[];
-    const int warp = threadIdx.x >> 5;
-    const int t = blockIdx.x * 4 + warp;
-    if (t >= a.T) return;
-    router_score_token<PER, LT>(a, t, group_scratch + warp * a.E);
-}
-
-// Scored router and grouping in one CTA, for few tokens: the warps' group
-// scratch and the grouping's table share the dynamic memory.
-template <int PER, typename LT>
-__global__ void __launch_bounds__(1024) router_score_route_small(const ScoreArgs a,
-                                                                 int32_t* __restrict__ m_indptr,
-                                                                 int32_t* __restrict__ perm,
-                                                                 int32_t* __restrict__ inv_perm,
-                                                                 int* status) {
-    extern __shared__ int tab[];
-    for (int t = threadIdx.x >> 5; t < a.T; t += 32)
-        router_score_token<PER, LT>(a, t, reinterpret_cast<float*>(tab) + (threadIdx.x >> 5) * a.E);
-    __syncthreads();
-    route_small_body(a.ids, a.T * a.k, a.E, m_indptr, perm, inv_perm, status, tab, true);
-}
-
-template <typename LT>
-int launch_score_t(const ScoreArgs& a, cudaStream_t s) {
-    const unsigned grid = static_cast<unsigned>((a.T + 3) / 4);
-    const size_t smem = a.n_group > 1 ? 4ull * a.E * sizeof(float) : 0;
-    if (a.E <= 128) router_score_kernel<4, LT><<<grid, 128, smem, s>>>(a);
-    else if (a.E <= 256) router_score_kernel<8, LT><<<grid, 128, smem, s>>>(a);
-    else if (a.E <= 512) router_score_kernel<16, LT><<<grid, 128, smem, s>>>(a);
-    else router_score_kernel<32, LT><<<grid, 128, smem, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
-}
-
-int launch_router_score(const ScoreArgs& a, cudaStream_t s) {
-    if (a.T == 0) return ST_OK;
-    return a.bf16 ? launch_score_t<__nv_bfloat16>(a, s) : launch_score_t<float>(a, s);
-}
-
-template <int PER, typename LT>
-int launch_score_route_inst(const ScoreArgs& a, const RouteArgs& r, cudaStream_t s) {
-    size_t smem = small_route_smem(a.T * a.k, a.E);
-    if (a.n_group > 1) smem = std::max<size_t>(smem, 32ull * a.E * sizeof(float));
-    // opt-in once per device and kernel; a second device just sets it again
-    static std::atomic<int> ready_dev{-1};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return ST_CUDA;
-    if (ready_dev.load() != dev) {
-        const int most = static_cast<int>(std::max<size_t>(kSmallRouteSmemMax, 32ull * 32 * PER * sizeof(float)));
-        if (cudaFuncSetAttribute(router_score_route_small<PER, LT>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
-            return ST_CUDA;
-        ready_dev.store(dev);
-    }
-    router_score_route_small<PER, LT><<<1, 1024, smem, s>>>(a, r.m_indptr, r.perm, r.inv_perm, r.status);
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
-}
-
-template <typename LT>
-int launch_score_route_t(const ScoreArgs& a, const RouteArgs& r, cudaStream_t s) {
-    if (a.E <= 128) return launch_score_route_inst<4, LT>(a, r, s);
-    if (a.E <= 256) return launch_score_route_inst<8, LT>(a, r, s);
-    if (a.E <= 512) return launch_score_route_inst<16, LT>(a, r, s);
-    return launch_score_route_inst<32, LT>(a, r, s);
-}
-
-// One launch for few tokens: a token costs its warp of the one CTA about as
-// much as a sixteenth of the launch it saves.
-constexpr int kScoreRouteTokens = 128;
-
-int launch_router_score_route(const ScoreArgs& a, const RouteArgs& r, cudaStream_t s) {
-    const int R = a.T * a.k;
-    if (a.T > 0 && a.T <= kScoreRouteTokens && route_single_launch(R))
-        return a.bf16 ? launch_score_route_t<__nv_bfloat16>(a, r, s) : launch_score_route_t<float>(a, r, s);
-    RouteArgs rr = r;
-    rr.clear_status = 1;
-    if (!route_single_launch(R) &&
-        cudaMemsetAsync(r.status, 0, sizeof(int) * kStatusInts, s) != cudaSuccess)
-        return ST_CUDA;
-    if (int st = launch_router_score(a, s)) return st;
-    return launch_route_permute(rr, s);
 }
 
 }  // namespace moe

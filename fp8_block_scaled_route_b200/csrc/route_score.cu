@@ -1,0 +1,817 @@
+// Scored router: expert choice by softmax or sigmoid scores, a selection bias,
+// expert groups and top-k, and the grouping of its pairs by expert.
+//
+// For token t, with x the logits and b the bias:
+//   p_e = 1 / (1 + exp(-x_e)) or softmax(x)_e;  c_e = p_e + b_e (the order of
+//   x without a bias);  group g = E / n_group consecutive experts, G_g = the
+//   sum of its group_top (1 or 2) largest c;  candidates: the topk_group
+//   groups with the largest G;  ids: the k largest c among them, descending,
+//   ties to the lower index;  w_j = p_j (/ sum p) * scale.
+// Masked experts (logit NaN or at most its type's lowest value, bias NaN or at
+// most -FLT_MAX) rank after every other, by index, and get weight 0.
+//
+// One warp per token, lane l holding experts l + 32 i.  Bound: integer and
+// compare instructions (8192 x 256 logits are 8 MB, 1.3 us of HBM), so the
+// selection avoids a warp-wide argmax per winner: the k-th largest of the 32
+// lane maxima bounds the k-th largest value from below, about k + 1 (k = 8) to
+// 1.4 k (k = 16) values reach that bound, and those, one per lane, find their
+// rank by comparing with one another.
+//
+// The choice is that of 64-bit values at 32-bit speed: c is computed in fp32
+// with a bounded error (score_tol).  Where two of the candidates lie closer
+// than the bound, the candidates' scores are computed again in 64 bits; where
+// the border between chosen and dropped groups is that close, or there are more
+// candidates than lanes (many equal values), the whole token is.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float kFltMax = 3.402823466e38f;
+constexpr float kBf16Lowest = -3.38953138925153547590e38f;
+constexpr int kNone = 0x7fffffff;
+
+__device__ __forceinline__ float ld_logit(const float* l, int e) { return l[e]; }
+__device__ __forceinline__ float ld_logit(const __nv_bfloat16* l, int e) {
+    return __bfloat162float(l[e]);
+}
+__device__ __forceinline__ bool logit_masked(const float*, float x) { return !(x > -kFltMax); }
+__device__ __forceinline__ bool logit_masked(const __nv_bfloat16*, float x) {
+    return !(x > kBf16Lowest);
+}
+
+// Order-preserving map of floats to unsigned integers above 0.
+__device__ __forceinline__ uint32_t order_key(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
+}
+
+// Bound on |difference of two fp32 selection values - the exact difference|,
+// v being one of them.  __expf is off by (2 + 1.173 |z|) ulps at argument z,
+// rcp.approx by one.
+//  sigmoid + b: p (1 - p) (2 + 1.173 |x|) + 1.5 ulps <= 1.1 * 2^-22 a score and
+//    one rounding of the sum; group values hold two scores: 2^-19 + 2^-21 |v|.
+//  softmax + b: p (2 + 1.7 d) e^-d ulps of the exponential, 24 ulps of a 37-term
+//    sum of such terms, and all p together are 1: 2^-17, the same relative part.
+//  no bias (group values, sums of scores): relative, with arguments up to 88
+//    (2 + 1.7 * 88) 2^-23 a side, 2^-14; below 1e-36 scores lose bits to
+//    underflow.
+__device__ __forceinline__ float score_tol(const ScoreArgs& a, float v) {
+    const float m = fabsf(v);
+    if (!a.bias) return 6.103515625e-05f * m + 1e-36f;
+    return (a.sigmoid ? 1.9073486328125e-06f : 7.62939453125e-06f) + 4.76837158203125e-07f * m;
+}
+
+__device__ __forceinline__ bool bias_masked(const ScoreArgs& a, int e) {
+    return a.bias && !(a.bias[e] > -kFltMax);
+}
+
+// Largest unmasked logit and sum of exp(x - largest) in 64 bits, for softmax.
+template <typename LT>
+__device__ __forceinline__ void softmax_f64(const ScoreArgs& a, const LT* l, double& mx, double& z) {
+    mx = -__longlong_as_double(0x7ff0000000000000ll);
+    z = 0.0;
+    const int lane = threadIdx.x & 31;
+    for (int e = lane; e < a.E; e += 32) {
+        const float x = ld_logit(l, e);
+        if (!logit_masked(l, x) && !bias_masked(a, e)) mx = fmax(mx, static_cast<double>(fminf(x, kFltMax)));
+    }
+    for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int e = lane; e < a.E; e += 32) {
+        const float x = ld_logit(l, e);
+        if (!logit_masked(l, x) && !bias_masked(a, e)) z += exp(static_cast<double>(fminf(x, kFltMax)) - mx);
+    }
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+}
+
+__device__ __forceinline__ double score_f64(const ScoreArgs& a, double x, double mx, double z) {
+    return a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - mx) / z;
+}
+
+// The whole choice with 64-bit scores; lane j < k returns the j-th expert.
+template <int PER, typename LT>
+__device__ __noinline__ int choose_f64(const ScoreArgs& a, const LT* l) {
+    const int lane = threadIdx.x & 31;
+    const int gs = a.E / a.n_group;
+    const double none = -__longlong_as_double(0x7ff0000000000000ll);
+    double mx = 0.0, z = 1.0;
+    if (!a.sigmoid) softmax_f64(a, l, mx, z);
+    // c: value the experts are ordered by; p: value that group sums add up
+    double c[PER], p[PER];
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        c[i] = p[i] = none;
+        if (e >= a.E) continue;
+        float x = ld_logit(l, e);
+        if (logit_masked(l, x) || bias_masked(a, e)) continue;
+        x = fminf(x, kFltMax);
+        const double s = score_f64(a, x, mx, z);
+        c[i] = a.bias ? s + static_cast<double>(fminf(a.bias[e], kFltMax)) : static_cast<double>(x);
+        p[i] = a.bias || a.group_top == 1 ? c[i] : s;
+    }
+    uint32_t groups = 1u;
+    if (a.n_group > 1) {
+        double mine = none;  // lane g: group g's value
+        for (int g = 0; g < a.n_group; ++g) {
+            double t1 = none, t2 = none;
+            for (int i = 0; i < PER; ++i) {
+                const int e = lane + 32 * i;
+                if (e < g * gs || e >= (g + 1) * gs) continue;
+                t2 = fmax(t2, fmin(t1, p[i]));
+                t1 = fmax(t1, p[i]);
+            }
+            for (int o = 16; o > 0; o >>= 1) {
+                const double u1 = __shfl_xor_sync(0xffffffffu, t1, o);
+                const double u2 = __shfl_xor_sync(0xffffffffu, t2, o);
+                t2 = fmax(fmin(t1, u1), fmax(t2, u2));
+                t1 = fmax(t1, u1);
+            }
+            const double v = a.group_top == 2 && t2 != none ? t1 + t2 : t1;
+            if (lane == g) mine = v;
+        }
+        int rank = 0;
+        for (int g = 0; g < a.n_group; ++g) {
+            const double v = __shfl_sync(0xffffffffu, mine, g);
+            rank += v > mine || (v == mine && g < lane) ? 1 : 0;
+        }
+        groups = __ballot_sync(0xffffffffu, lane < a.n_group && rank < a.topk_group);
+    }
+    uint32_t gone = 0;
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        if (e >= a.E || !((groups >> (e / gs)) & 1u)) gone |= 1u << i;
+    }
+    int chosen = 0;
+    for (int j = 0; j < a.k; ++j) {
+        double bv = none;
+        int be = kNone;
+        for (int i = 0; i < PER; ++i) {
+            if ((gone >> i) & 1u) continue;
+            if (be == kNone || c[i] > bv) {
+                bv = c[i];
+                be = lane + 32 * i;
+            }
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double ov = __shfl_xor_sync(0xffffffffu, bv, o);
+            const int oe = __shfl_xor_sync(0xffffffffu, be, o);
+            if (oe != kNone && (be == kNone || ov > bv || (ov == bv && oe < be))) {
+                bv = ov;
+                be = oe;
+            }
+        }
+        if (lane == (be & 31)) gone |= 1u << (be >> 5);
+        if (lane == j) chosen = be;
+    }
+    return chosen;
+}
+
+// Ranks of the m candidates in scratch (their experts ascending at ids[]) by
+// 64-bit values, lane l's candidates being l and l + 32.
+template <int CPL, typename LT>
+__device__ __noinline__ void rank_f64(const ScoreArgs& a, const LT* l, const int* ids, int m, double* c,
+                                      int (&rank)[CPL]) {
+    const int lane = threadIdx.x & 31;
+    double mx = 0.0, z = 1.0;
+    if (!a.sigmoid) softmax_f64(a, l, mx, z);
+    for (int q = 0; q < CPL; ++q)
+        if (lane + 32 * q < m) {
+            const int e = ids[lane + 32 * q];
+            const float x = fminf(ld_logit(l, e), kFltMax);
+            c[lane + 32 * q] =
+                score_f64(a, x, mx, z) + static_cast<double>(fminf(a.bias[e], kFltMax));
+        }
+    __syncwarp();
+    for (int q = 0; q < CPL; ++q) {
+        rank[q] = 0;
+        const int i = lane + 32 * q;
+        const double mine = i < m ? c[i] : 0.0;
+        for (int j = 0; j < m; ++j) rank[q] += c[j] > mine || (c[j] == mine && j < i) ? 1 : 0;
+    }
+}
+
+// Scratch of a warp: the group scan's E floats, then the candidates' values,
+// experts and 64-bit values.
+template <int CPL>
+__host__ __device__ constexpr int scratch_floats(int E, bool groups) {
+    return groups && E > 4 * 32 * CPL ? (E + 3) & ~3 : 4 * 32 * CPL;   // 16-byte aligned
+}
+
+// One token by one warp.  k <= 16 CPL.  hist: the CTA's expert counts, or null.
+template <int PER, int CPL, typename LT>
+__device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* scratch, int* hist) {
+    const int lane = threadIdx.x & 31;
+    const LT* l = static_cast<const LT*>(a.logits) + static_cast<long long>(t) * a.E;
+    const bool sums = a.n_group > 1 && a.group_top == 2;   // group values add scores up
+    const bool need_score = a.bias != nullptr || sums;
+    const bool need_z = !a.sigmoid && (need_score || !a.renorm);
+    const float ninf = -INFINITY;
+    // v: logits, then selection values; -inf where masked or no expert
+    float v[PER], g[PER];
+    bool any_masked = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        v[i] = e < a.E ? ld_logit(l, e) : ninf;
+        g[i] = a.bias && e < a.E ? a.bias[e] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool m = logit_masked(l, v[i]) || !(g[i] > -kFltMax);
+        any_masked |= m && lane + 32 * i < a.E;
+        v[i] = m ? ninf : fminf(v[i], kFltMax);
+    }
+    float mx = 0.0f, zinv = 0.0f;
+    if (need_z) {
+        float m = v[0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) m = fmaxf(m, v[i]);
+        mx = key_value(__reduce_max_sync(0xffffffffu, order_key(m)));
+        if (mx == ninf) mx = 0.0f;   // nothing unmasked: every term below is 0
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) z += __expf(v[i] - mx);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        zinv = z > 0.0f ? __frcp_rn(z) : 0.0f;
+    }
+    if (need_score) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool live = v[i] > ninf;
+            const float s = a.sigmoid ? rcp_approx(1.0f + __expf(-v[i])) : __expf(v[i] - mx) * zinv;
+            if (a.bias) {
+                v[i] = live ? s + fminf(g[i], kFltMax) : ninf;
+                g[i] = v[i];
+            } else {
+                g[i] = live ? s : ninf;
+            }
+        }
+    }
+    bool whole = false;           // decide the whole token in 64 bits
+    if (a.n_group > 1) {
+        const int gs = a.E / a.n_group;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (lane + 32 * i < a.E) scratch[lane + 32 * i] = need_score ? g[i] : v[i];
+        __syncwarp();
+        // 2^lp lanes scan a group together (2^lp * n_group <= 32), then merge
+        const int lp = a.n_group > 16 ? 0 : a.n_group > 8 ? 1 : a.n_group > 4 ? 2 : a.n_group > 2 ? 3 : 4;
+        const int grp = lane >> lp;
+        float t1 = ninf, t2 = ninf;
+        if (grp < a.n_group)
+            for (int i = lane & ((1 << lp) - 1); i < gs; i += 1 << lp) {
+                const float f = scratch[grp * gs + i];
+                t2 = fmaxf(t2, fminf(t1, f));
+                t1 = fmaxf(t1, f);
+            }
+        for (int o = (1 << lp) >> 1; o > 0; o >>= 1) {
+            const float u1 = __shfl_xor_sync(0xffffffffu, t1, o);
+            const float u2 = __shfl_xor_sync(0xffffffffu, t2, o);
+            t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
+            t1 = fmaxf(t1, u1);
+        }
+        const float gv = a.group_top == 2 && t2 > ninf ? t1 + t2 : t1;
+        // the group's rank, by the group's first lane's value
+        int rank = 0;
+        for (int o = 0; o < a.n_group; ++o) {
+            const float ov = __shfl_sync(0xffffffffu, gv, o << lp);
+            rank += ov > gv || (ov == gv && o < grp) ? 1 : 0;
+        }
+        const bool in = grp < a.n_group && rank < a.topk_group;
+        const uint32_t lanes_in = __ballot_sync(0xffffffffu, in);
+        if (need_score && a.topk_group < a.n_group) {
+            const bool live = grp < a.n_group && gv > ninf;
+            const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(gv) : 0xffffffffu);
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(gv) : 0u);
+            if (lo != 0xffffffffu && hi != 0u) {
+                const float fl = key_value(lo), fh = key_value(hi);
+                whole = !(fl - fh > fmaxf(score_tol(a, fl), score_tol(a, fh)));
+            }
+        }
+        // e / gs = e * inv_gs >> 20 for e, gs <= 1024
+        const uint32_t inv_gs = ((1u << 20) + gs - 1) / gs;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.E && !((lanes_in >> (((e * inv_gs) >> 20) << lp)) & 1u)) v[i] = ninf;
+        }
+        __syncwarp();
+    }
+    if (__any_sync(0xffffffffu, any_masked)) {
+        // masked experts are chosen only where too few others are left
+        int live = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) live += v[i] > ninf ? 1 : 0;
+        whole = whole || __reduce_add_sync(0xffffffffu, live) < a.k;
+    }
+    // the k-th largest of the lanes' maxima (CPL of each lane)
+    float top[CPL];
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) {
+        top[q] = v[q * (PER / CPL)];
+#pragma unroll
+        for (int i = 1; i < PER / CPL; ++i) top[q] = fmaxf(top[q], v[q * (PER / CPL) + i]);
+    }
+    uint32_t cur[CPL], kth;
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) cur[q] = top[q] > ninf ? order_key(top[q]) : 0u;
+    int seen = 0;
+    do {
+        uint32_t m = cur[0];
+        if constexpr (CPL == 2) m = max(m, cur[1]);
+        kth = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+            const bool eq = cur[q] == kth;
+            seen += __popc(__ballot_sync(0xffffffffu, eq));
+            if (eq) cur[q] = 0u;
+        }
+    } while (seen < a.k && kth != 0u);
+    float bound = kth != 0u ? key_value(kth) : ninf;
+    if (a.bias && kth != 0u) bound -= score_tol(a, bound);
+    // candidates, in ascending expert order
+    float* cv = scratch;
+    int* ce = reinterpret_cast<int*>(scratch) + 32 * CPL;
+    int m = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool pass = v[i] >= bound && v[i] > ninf;
+        const uint32_t who = __ballot_sync(0xffffffffu, pass);
+        if (who) {
+            const int at = m + __popc(who & ((1u << lane) - 1u));
+            if (pass && at < 32 * CPL) {
+                cv[at] = v[i];
+                ce[at] = lane + 32 * i;
+            }
+            m += __popc(who);
+        }
+    }
+    whole = whole || m > 32 * CPL;
+    int expert[CPL], rank[CPL];
+    if (!whole) {
+#pragma unroll
+        for (int q = 0; q < CPL; ++q)
+            if (lane + 32 * q >= m) cv[lane + 32 * q] = ninf;
+        __syncwarp();
+        float mine[CPL], tol[CPL];
+        bool close = false;
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+            const int i = lane + 32 * q;
+            mine[q] = cv[i];
+            expert[q] = i < m ? ce[i] : 0;
+            rank[q] = 0;
+            tol[q] = a.bias && i < m ? score_tol(a, mine[q]) : -1.0f;
+        }
+        for (int j = 0; j < m; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(cv + j);
+            const float o[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int q = 0; q < CPL; ++q) {
+                    const int i = lane + 32 * q;
+                    rank[q] += o[u] > mine[q] || (o[u] == mine[q] && j + u < i) ? 1 : 0;
+                    close |= j + u != i && fabsf(o[u] - mine[q]) <= tol[q];   // padding: inf or NaN
+                }
+        }
+        if (a.bias && __any_sync(0xffffffffu, close)) {
+            double* cd = reinterpret_cast<double*>(scratch + 2 * 32 * CPL);
+            rank_f64<CPL, LT>(a, l, ce, m, cd, rank);
+        }
+#pragma unroll
+        for (int q = 0; q < CPL; ++q)
+            if (lane + 32 * q >= m) rank[q] = kNone;
+    } else {
+        expert[0] = choose_f64<PER, LT>(a, l);
+        rank[0] = lane;
+        if constexpr (CPL == 2) rank[1] = kNone;
+    }
+    __syncwarp();   // the scratch is free for the warp's next token
+    // weights of the k winners
+    float x[CPL], u[CPL];
+    bool on[CPL];
+#pragma unroll
+    for (int q = 0; q < CPL; ++q) {
+        on[q] = false;
+        x[q] = 0.0f;
+        if (rank[q] < a.k) {
+            x[q] = ld_logit(l, expert[q]);
+            on[q] = !logit_masked(l, x[q]) && !bias_masked(a, expert[q]);
+            x[q] = fminf(x[q], kFltMax);
+        }
+    }
+    if (a.renorm) {
+        // scaled by the largest so that no row of small scores underflows
+        uint32_t xk = 0u;
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) xk = max(xk, on[q] ? order_key(x[q]) : 0u);
+        xk = __reduce_max_sync(0xffffffffu, xk);
+        float big = xk ? key_value(xk) : 0.0f;
+        if (a.sigmoid) big = fminf(big, 0.0f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+            u[q] = 0.0f;
+            if (on[q])
+                u[q] = !a.sigmoid ? expf(x[q] - big)
+                                  : __fdiv_rn(x[q] > 0.0f ? 1.0f : expf(x[q] - big), 1.0f + expf(x[q] > 0.0f ? -x[q] : x[q]));
+            sum += u[q];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) u[q] = sum > 0.0f ? __fdiv_rn(u[q], sum) : 0.0f;
+    } else {
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) {
+            u[q] = 0.0f;
+            if (on[q])
+                u[q] = !a.sigmoid ? expf(x[q] - mx) * zinv
+                                  : __fdiv_rn(x[q] > 0.0f ? 1.0f : expf(x[q]), 1.0f + expf(x[q] > 0.0f ? -x[q] : x[q]));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < CPL; ++q)
+        if (rank[q] < a.k) {
+            const long long at = static_cast<long long>(t) * a.k + rank[q];
+            a.ids[at] = expert[q];
+            a.w[at] = u[q] * a.scale;
+            if (hist) atomicAdd(&hist[expert[q]], 1);
+        }
+}
+
+constexpr int kScoreWarps = 4;
+
+template <int PER, int CPL, typename LT>
+__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs a) {
+    extern __shared__ __align__(16) float scratch[];
+    const int warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kScoreWarps + warp;
+    if (t >= a.T) return;
+    score_token<PER, CPL, LT>(a, t, scratch + warp * scratch_floats<CPL>(a.E, a.n_group > 1), nullptr);
+}
+
+// ------------------------------------------------------------ grouping
+// Stable grouping of n consecutive pairs by expert in one CTA of NW warps.
+// Each warp owns a segment of the pairs and ranks each pair among the earlier
+// ones of its segment (one ballot per expert-id bit gives the lanes with the
+// same expert); a thread per expert then scans the segments' counts.
+//   cnt   shared [NW][E], zeroed
+//   base  shared [E]: first output row of each expert (filled by `first_rows`
+//         from the experts' counts, which it gets for all E experts)
+constexpr int kSteps = 9;   // most 32-pair steps of a segment
+
+template <int NW>
+struct Segment {
+    int p0, n;             // this warp's pairs: p0 + [0, n)
+    int e[kSteps], r[kSteps];
+};
+
+template <int NW>
+__device__ __forceinline__ void count_pairs(Segment<NW>& s, const int32_t* ids, int first, int n, int E,
+                                            int nbits, int* cnt) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = ((n + NW - 1) / NW + 31) & ~31;
+    s.p0 = first + min(n, warp * per);
+    s.n = min(per, n - min(n, warp * per));
+    int* c = cnt + warp * E;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int p = i * 32 + lane;
+        s.e[i] = p < s.n ? __ldcg(ids + s.p0 + p) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        if (i * 32 >= s.n) break;
+        const bool ok = s.e[i] >= 0;
+        unsigned peers = __ballot_sync(0xffffffffu, ok);
+        for (int b = 0; b < nbits; ++b) {
+            const bool bit = (s.e[i] >> b) & 1;
+            const unsigned bb = __ballot_sync(0xffffffffu, bit);
+            peers &= bit ? bb : ~bb;
+        }
+        const int before = ok ? c[s.e[i]] : 0;
+        s.r[i] = before + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (ok && (peers & ((1u << lane) - 1u)) == 0) c[s.e[i]] = before + __popc(peers);
+        __syncwarp();
+    }
+}
+
+template <int NW>
+__device__ __forceinline__ void place_pairs(const Segment<NW>& s, int E, const int* cnt, const int* base,
+                                            int32_t* perm, int32_t* inv_perm) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int p = i * 32 + lane;
+        if (p < s.n) {
+            const int row = base[s.e[i]] + cnt[warp * E + s.e[i]] + s.r[i];
+            perm[row] = s.p0 + p;
+            if (inv_perm) inv_perm[s.p0 + p] = row;
+        }
+    }
+}
+
+// Exclusive scan over the CTA's threads (NW warps) of one value each.
+template <int NW>
+__device__ __forceinline__ int cta_exclusive(int v, int* warp_tot) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) warp_tot[warp] = incl;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < NW; ++w) before += w < warp ? warp_tot[w] : 0;
+    return before + incl - v;
+}
+
+__host__ __device__ inline int bits_of(int E) {
+    int n = 0;
+    while ((1 << n) < E) ++n;
+    return n;
+}
+
+// Few tokens: the scored router over a cluster of 8 CTAs (a warp per token for
+// up to 128 tokens), then the grouping in the cluster's first CTA.  One launch;
+// one CTA alone would issue 64 tokens' selection in ~6 us.
+constexpr int kSmallWarps = 16;
+constexpr int kSmallCluster = 8;
+constexpr int kSmallTokens = 256;
+constexpr int kSmallPairs = kSmallWarps * kSteps * 32;
+
+template <int PER, int CPL, typename LT>
+__global__ void __launch_bounds__(32 * kSmallWarps)
+    score_route_small(const ScoreArgs a, int32_t* m_indptr, int32_t* perm, int32_t* inv_perm,
+                      int* status, const int nbits) {
+    extern __shared__ __align__(16) float scratch[];
+    __shared__ int warp_tot[kSmallWarps];
+    const int warp = threadIdx.x >> 5;
+    const uint32_t rank = cluster_ctarank();
+    const int sf = scratch_floats<CPL>(a.E, a.n_group > 1);
+    int* cnt = reinterpret_cast<int*>(scratch + kSmallWarps * sf);   // [warps][E]
+    int* base = cnt + kSmallWarps * a.E;                             // [E]
+    if (rank == 0) {
+        for (int i = threadIdx.x; i < kSmallWarps * a.E; i += 32 * kSmallWarps) cnt[i] = 0;
+        if (threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
+    }
+    for (int t = rank + kSmallCluster * warp; t < a.T; t += kSmallCluster * kSmallWarps)
+        score_token<PER, CPL, LT>(a, t, scratch + warp * sf, nullptr);
+    __syncwarp();
+    cluster_sync_all();      // every CTA's ids are visible
+    if (rank != 0) return;
+    const int R = a.T * a.k;
+    Segment<kSmallWarps> seg;
+    count_pairs(seg, a.ids, 0, R, a.E, nbits, cnt);
+    __syncthreads();
+    // experts [e0, e1) of this thread: counts of the segments before, totals
+    const int ept = (a.E + 32 * kSmallWarps - 1) / (32 * kSmallWarps);
+    const int e0 = min(a.E, static_cast<int>(threadIdx.x) * ept), e1 = min(a.E, e0 + ept);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        int run = 0, c[kSmallWarps];
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) c[w] = cnt[w * a.E + e];
+#pragma unroll
+        for (int w = 0; w < kSmallWarps; ++w) {
+            cnt[w * a.E + e] = run;
+            run += c[w];
+        }
+        base[e] = run;
+        sum += run;
+    }
+    int first = cta_exclusive<kSmallWarps>(sum, warp_tot);
+    for (int e = e0; e < e1; ++e) {
+        const int n = base[e];
+        base[e] = first;
+        m_indptr[e] = first;
+        first += n;
+    }
+    if (threadIdx.x == 0) m_indptr[a.E] = R;
+    __syncthreads();
+    place_pairs(seg, a.E, cnt, base, perm, inv_perm);
+}
+
+// More tokens, first launch: a cluster of CTAs routes one chunk of tokens
+// (about 1024 pairs) and writes the chunk's expert counts.
+constexpr int kChunkWarps = 8;
+constexpr int kMaxChunks = 128;
+
+template <int PER, int CPL, typename LT>
+__global__ void __launch_bounds__(32 * kChunkWarps)
+    score_count_kernel(const ScoreArgs a, int32_t* chunk_hist, int* status, const int chunk_tokens,
+                       const int C) {
+    extern __shared__ __align__(16) float scratch[];
+    const int warp = threadIdx.x >> 5;
+    const int sf = scratch_floats<CPL>(a.E, a.n_group > 1);
+    int* hist = reinterpret_cast<int*>(scratch + kChunkWarps * sf);
+    const int chunk = blockIdx.x / C, rank = blockIdx.x - chunk * C;
+    for (int e = threadIdx.x; e < a.E; e += 32 * kChunkWarps) hist[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
+    __syncthreads();
+    const int t1 = min(a.T, (chunk + 1) * chunk_tokens);
+    for (int t = chunk * chunk_tokens + rank * kChunkWarps + warp; t < t1; t += C * kChunkWarps)
+        score_token<PER, CPL, LT>(a, t, scratch + warp * sf, hist);
+    __syncwarp();
+    cluster_sync_all();
+    for (int e = rank * 32 * kChunkWarps + threadIdx.x; e < a.E; e += C * 32 * kChunkWarps) {
+        int n = 0;
+        for (int r = 0; r < C; ++r) n += ld_shared_cluster_s32(mapa_shared(smem_u32(hist + e), r));
+        chunk_hist[static_cast<long long>(chunk) * a.E + e] = n;
+    }
+    __syncwarp();
+    cluster_sync_all();      // peers have read this CTA's counts
+}
+
+// Second launch: one CTA per chunk adds up the counts of the chunks before it
+// (every CTA for itself: at most 128 rows of counts out of L2) and places its
+// pairs.
+template <int EPT>
+__global__ void __launch_bounds__(32 * kChunkWarps)
+    place_kernel(const int32_t* __restrict__ ids, int R, int E, int nbits, int chunk_pairs,
+                 const int32_t* __restrict__ chunk_hist, int32_t* m_indptr, int32_t* perm,
+                 int32_t* inv_perm) {
+    extern __shared__ __align__(16) int smem[];
+    __shared__ int warp_tot[kChunkWarps];
+    int* cnt = smem;                       // [warps][E]
+    int* base = cnt + kChunkWarps * E;     // [E]
+    const int nchunks = gridDim.x, chunk = blockIdx.x;
+    for (int i = threadIdx.x; i < kChunkWarps * E; i += 32 * kChunkWarps) cnt[i] = 0;
+    __syncthreads();
+    const int first = chunk * chunk_pairs;
+    Segment<kChunkWarps> seg;
+    count_pairs(seg, ids, first, min(chunk_pairs, R - first), E, nbits, cnt);
+    // experts EPT * thread + i: pairs in all chunks and in the chunks before
+    const int e0 = threadIdx.x * EPT;
+    int total[EPT] = {}, before[EPT] = {};
+    for (int c0 = 0; c0 < nchunks; c0 += 16) {
+        int h[16][EPT];
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                h[c][i] = c0 + c < nchunks && e0 + i < E
+                              ? chunk_hist[static_cast<long long>(c0 + c) * E + e0 + i] : 0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {
+                if (c0 + c < chunk) before[i] += h[c][i];
+                total[i] += h[c][i];
+            }
+    }
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) sum += total[i];
+    __syncthreads();                       // every warp's counts are in cnt
+    int row = cta_exclusive<kChunkWarps>(sum, warp_tot);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+        const int e = e0 + i;
+        if (e < E) {
+            base[e] = row + before[i];
+            if (chunk == 0) m_indptr[e] = row;
+            row += total[i];
+            int run = 0;
+#pragma unroll
+            for (int w = 0; w < kChunkWarps; ++w) {
+                const int n = cnt[w * E + e];
+                cnt[w * E + e] = run;
+                run += n;
+            }
+        }
+    }
+    if (chunk == 0 && threadIdx.x == 0) m_indptr[E] = R;
+    __syncthreads();
+    place_pairs(seg, E, cnt, base, perm, inv_perm);
+}
+
+// ------------------------------------------------------------ launches
+// Opt-in of a kernel to `bytes` of dynamic shared memory, once per device and
+// kernel; `ready_dev` is the kernel's own (alternating devices set it again).
+template <typename Kern>
+bool smem_ready(Kern kern, size_t bytes, std::atomic<int>& ready_dev) {
+    if (bytes <= 48 * 1024) return true;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (ready_dev.load() == dev) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess)
+        return false;
+    ready_dev.store(dev);
+    return true;
+}
+
+template <typename... Args>
+int launch_cluster(void (*kern)(Args...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
+                   cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ST_OK : ST_CUDA;
+}
+
+int launch_place(const RouteArgs& r, int chunk_pairs, int nchunks, cudaStream_t s) {
+    const size_t smem = static_cast<size_t>(kChunkWarps + 1) * r.E * sizeof(int);
+    const int R = r.T * r.k, nb = bits_of(r.E);
+    if (r.E <= 32 * kChunkWarps)
+        place_kernel<1><<<nchunks, 32 * kChunkWarps, smem, s>>>(r.topk_ids, R, r.E, nb, chunk_pairs,
+                                                                r.chunk_hist, r.m_indptr, r.perm, r.inv_perm);
+    else
+        place_kernel<4><<<nchunks, 32 * kChunkWarps, smem, s>>>(r.topk_ids, R, r.E, nb, chunk_pairs,
+                                                                r.chunk_hist, r.m_indptr, r.perm, r.inv_perm);
+    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+}
+
+template <int PER, int CPL, typename LT>
+int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
+    const size_t sf = scratch_floats<CPL>(a.E, a.n_group > 1) * sizeof(float);
+    const int R = a.T * a.k;
+    if (r && a.T <= kSmallTokens && R <= kSmallPairs) {
+        static std::atomic<int> ready{-1};
+        const size_t smem = kSmallWarps * sf + (kSmallWarps + 1ull) * a.E * sizeof(int);
+        auto kern = score_route_small<PER, CPL, LT>;
+        if (!smem_ready(kern, smem, ready)) return ST_CUDA;
+        return launch_cluster(kern, kSmallCluster, 32 * kSmallWarps, kSmallCluster, smem, s, a, r->m_indptr,
+                              r->perm, r->inv_perm, r->status, static_cast<const int>(bits_of(a.E)));
+    }
+    // chunks of whole tokens, at least kRouteChunk pairs each, so that their
+    // counts fit the workspace's
+    const int chunk_tokens = (kRouteChunk + a.k - 1) / a.k;
+    const int nchunks = (a.T + chunk_tokens - 1) / chunk_tokens;
+    if (r && nchunks <= kMaxChunks && a.k >= 2) {
+        static std::atomic<int> ready{-1};
+        const size_t smem = kChunkWarps * sf + static_cast<size_t>(a.E) * sizeof(int);
+        const int C = a.k >= 8 ? 4 : 8;
+        auto kern = score_count_kernel<PER, CPL, LT>;
+        if (!smem_ready(kern, smem, ready)) return ST_CUDA;
+        const int st = launch_cluster(kern, nchunks * C, 32 * kChunkWarps, C, smem, s, a, r->chunk_hist,
+                                      r->status, chunk_tokens, C);
+        return st ? st : launch_place(*r, chunk_tokens * a.k, nchunks, s);
+    }
+    if (a.T > 0) {
+        static std::atomic<int> ready{-1};
+        auto kern = score_kernel<PER, CPL, LT>;
+        if (!smem_ready(kern, kScoreWarps * sf, ready)) return ST_CUDA;
+        kern<<<static_cast<unsigned>((a.T + kScoreWarps - 1) / kScoreWarps), 32 * kScoreWarps,
+               kScoreWarps * sf, s>>>(a);
+        if (cudaGetLastError() != cudaSuccess) return ST_CUDA;
+    }
+    if (!r) return ST_OK;
+    RouteArgs rr = *r;
+    rr.clear_status = 1;
+    if (!route_single_launch(R) &&
+        cudaMemsetAsync(r->status, 0, sizeof(int) * kStatusInts, s) != cudaSuccess)
+        return ST_CUDA;
+    return launch_route_permute(rr, s);
+}
+
+template <int PER, typename LT>
+int launch_k(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
+    return a.k <= 16 ? launch_inst<PER, 1, LT>(a, r, s) : launch_inst<PER, 2, LT>(a, r, s);
+}
+
+template <typename LT>
+int launch_e(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
+    if (a.E <= 128) return launch_k<4, LT>(a, r, s);
+    if (a.E <= 256) return launch_k<8, LT>(a, r, s);
+    if (a.E <= 512) return launch_k<16, LT>(a, r, s);
+    return launch_k<32, LT>(a, r, s);
+}
+
+}  // namespace
+
+int launch_router_score(const ScoreArgs& a, cudaStream_t s) {
+    if (a.T == 0) return ST_OK;
+    return a.bf16 ? launch_e<__nv_bfloat16>(a, nullptr, s) : launch_e<float>(a, nullptr, s);
+}
+
+int launch_router_score_route(const ScoreArgs& a, const RouteArgs& r, cudaStream_t s) {
+    return a.bf16 ? launch_e<__nv_bfloat16>(a, &r, s) : launch_e<float>(a, &r, s);
+}
+
+}  // namespace moe
