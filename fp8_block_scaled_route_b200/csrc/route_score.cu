@@ -19,9 +19,10 @@
 //
 // The choice is that of 64-bit values at 32-bit speed: c is computed in fp32
 // with a bounded error (score_tol).  Where two of the candidates lie closer
-// than the bound, the candidates' scores are computed again in 64 bits; where
-// the border between chosen and dropped groups is that close, or there are more
-// candidates than lanes (many equal values), the whole token is.
+// than the bound, the candidates' scores are computed again in 64 bits, where the
+// border between chosen and dropped groups is that close, the groups'; where
+// there are more candidates than places (many equal values) or fewer unmasked
+// experts than k, the whole token is decided in 64 bits.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -74,6 +75,12 @@ __device__ __forceinline__ float score_tol(const ScoreArgs& a, float v) {
 
 __device__ __forceinline__ bool bias_masked(const ScoreArgs& a, int e) {
     return a.bias && !(a.bias[e] > -kFltMax);
+}
+
+// exp(x - big) (softmax), or sigmoid(x) / exp(big) (big <= 0, and 0 where x > 0).
+__device__ __forceinline__ float score_over(const ScoreArgs& a, float x, float big) {
+    if (!a.sigmoid) return expf(x - big);
+    return (x > 0.0f ? 1.0f : expf(x - big)) * rcp_approx(1.0f + expf(-fabsf(x)));
 }
 
 // Largest unmasked logit and sum of exp(x - largest) in 64 bits, for softmax.
@@ -176,6 +183,64 @@ __device__ __noinline__ int choose_f64(const ScoreArgs& a, const LT* l) {
     return chosen;
 }
 
+// Log2 of the lanes that scan a group together.
+__device__ __forceinline__ int group_lanes_log2(int n_group) {
+    return n_group > 16 ? 0 : n_group > 8 ? 1 : n_group > 4 ? 2 : n_group > 2 ? 3 : 4;
+}
+
+// Group values and ranks from the E selection values in scratch (-inf where
+// masked): lane's group is lane >> lp; gv its value, returns its rank.
+template <typename T>
+__device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch, T& gv) {
+    const int lane = threadIdx.x & 31;
+    const int lp = group_lanes_log2(a.n_group), gs = a.E / a.n_group;
+    const int grp = lane >> lp;
+    const T ninf = -static_cast<T>(INFINITY);
+    T t1 = ninf, t2 = ninf;
+    if (grp < a.n_group)
+        for (int i = lane & ((1 << lp) - 1); i < gs; i += 1 << lp) {
+            const T f = scratch[grp * gs + i];
+            t2 = max(t2, min(t1, f));
+            t1 = max(t1, f);
+        }
+    for (int o = (1 << lp) >> 1; o > 0; o >>= 1) {
+        const T u1 = __shfl_xor_sync(0xffffffffu, t1, o);
+        const T u2 = __shfl_xor_sync(0xffffffffu, t2, o);
+        t2 = max(min(t1, u1), max(t2, u2));
+        t1 = max(t1, u1);
+    }
+    gv = a.group_top == 2 && t2 > ninf ? t1 + t2 : t1;
+    int rank = 0;
+    for (int o = 0; o < a.n_group; ++o) {
+        const T ov = __shfl_sync(0xffffffffu, gv, o << lp);
+        rank += ov > gv || (ov == gv && o < grp) ? 1 : 0;
+    }
+    return rank;
+}
+
+// Lanes whose group is chosen, by 64-bit values; scratch: E doubles.
+template <typename LT>
+__device__ __noinline__ uint32_t choose_groups_f64(const ScoreArgs& a, const LT* l, double* scratch) {
+    const int lane = threadIdx.x & 31;
+    double mx = 0.0, z = 1.0;
+    if (!a.sigmoid) softmax_f64(a, l, mx, z);
+    __syncwarp();
+    for (int e = lane; e < a.E; e += 32) {
+        const float x = ld_logit(l, e);
+        double s = -static_cast<double>(INFINITY);
+        if (!logit_masked(l, x) && !bias_masked(a, e)) {
+            s = score_f64(a, fminf(x, kFltMax), mx, z);
+            if (a.bias) s += static_cast<double>(fminf(a.bias[e], kFltMax));
+        }
+        scratch[e] = s;
+    }
+    __syncwarp();
+    double gv;
+    const int rank = rank_groups(a, scratch, gv);
+    const int grp = lane >> group_lanes_log2(a.n_group);
+    return __ballot_sync(0xffffffffu, grp < a.n_group && rank < a.topk_group);
+}
+
 // Ranks of the m candidates in scratch (their experts ascending at ids[]) by
 // 64-bit values, lane l's candidates being l and l + 32.
 template <int CPL, typename LT>
@@ -200,11 +265,11 @@ __device__ __noinline__ void rank_f64(const ScoreArgs& a, const LT* l, const int
     }
 }
 
-// Scratch of a warp: the group scan's E floats, then the candidates' values,
-// experts and 64-bit values.
+// Scratch of a warp: the group scan's E values (fp32, or 64-bit where they are
+// close), then the candidates' values, experts and 64-bit values.
 template <int CPL>
 __host__ __device__ constexpr int scratch_floats(int E, bool groups) {
-    return groups && E > 4 * 32 * CPL ? (E + 3) & ~3 : 4 * 32 * CPL;   // 16-byte aligned
+    return groups && 2 * E > 4 * 32 * CPL ? (2 * E + 3) & ~3 : 4 * 32 * CPL;   // 16-byte aligned
 }
 
 // One token by one warp.  k <= 16 CPL.  hist: the CTA's expert counts, or null.
@@ -218,7 +283,6 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
     const float ninf = -INFINITY;
     // v: logits, then selection values; -inf where masked or no expert
     float v[PER], g[PER];
-    bool any_masked = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int e = lane + 32 * i;
@@ -228,7 +292,6 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const bool m = logit_masked(l, v[i]) || !(g[i] > -kFltMax);
-        any_masked |= m && lane + 32 * i < a.E;
         v[i] = m ? ninf : fminf(v[i], kFltMax);
     }
     float mx = 0.0f, zinv = 0.0f;
@@ -258,45 +321,26 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
             }
         }
     }
-    bool whole = false;           // decide the whole token in 64 bits
     if (a.n_group > 1) {
         const int gs = a.E / a.n_group;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             if (lane + 32 * i < a.E) scratch[lane + 32 * i] = need_score ? g[i] : v[i];
         __syncwarp();
-        // 2^lp lanes scan a group together (2^lp * n_group <= 32), then merge
-        const int lp = a.n_group > 16 ? 0 : a.n_group > 8 ? 1 : a.n_group > 4 ? 2 : a.n_group > 2 ? 3 : 4;
-        const int grp = lane >> lp;
-        float t1 = ninf, t2 = ninf;
-        if (grp < a.n_group)
-            for (int i = lane & ((1 << lp) - 1); i < gs; i += 1 << lp) {
-                const float f = scratch[grp * gs + i];
-                t2 = fmaxf(t2, fminf(t1, f));
-                t1 = fmaxf(t1, f);
-            }
-        for (int o = (1 << lp) >> 1; o > 0; o >>= 1) {
-            const float u1 = __shfl_xor_sync(0xffffffffu, t1, o);
-            const float u2 = __shfl_xor_sync(0xffffffffu, t2, o);
-            t2 = fmaxf(fminf(t1, u1), fmaxf(t2, u2));
-            t1 = fmaxf(t1, u1);
-        }
-        const float gv = a.group_top == 2 && t2 > ninf ? t1 + t2 : t1;
-        // the group's rank, by the group's first lane's value
-        int rank = 0;
-        for (int o = 0; o < a.n_group; ++o) {
-            const float ov = __shfl_sync(0xffffffffu, gv, o << lp);
-            rank += ov > gv || (ov == gv && o < grp) ? 1 : 0;
-        }
+        // the lanes of a group (2^lp of them, 2^lp * n_group <= 32) scan it together
+        const int lp = group_lanes_log2(a.n_group), grp = lane >> lp;
+        float gv;
+        const int rank = rank_groups(a, scratch, gv);
         const bool in = grp < a.n_group && rank < a.topk_group;
-        const uint32_t lanes_in = __ballot_sync(0xffffffffu, in);
+        uint32_t lanes_in = __ballot_sync(0xffffffffu, in);
         if (need_score && a.topk_group < a.n_group) {
             const bool live = grp < a.n_group && gv > ninf;
             const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(gv) : 0xffffffffu);
             const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(gv) : 0u);
             if (lo != 0xffffffffu && hi != 0u) {
                 const float fl = key_value(lo), fh = key_value(hi);
-                whole = !(fl - fh > fmaxf(score_tol(a, fl), score_tol(a, fh)));
+                if (!(fl - fh > fmaxf(score_tol(a, fl), score_tol(a, fh))))
+                    lanes_in = choose_groups_f64(a, l, reinterpret_cast<double*>(scratch));
             }
         }
         // e / gs = e * inv_gs >> 20 for e, gs <= 1024
@@ -307,13 +351,6 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
             if (e < a.E && !((lanes_in >> (((e * inv_gs) >> 20) << lp)) & 1u)) v[i] = ninf;
         }
         __syncwarp();
-    }
-    if (__any_sync(0xffffffffu, any_masked)) {
-        // masked experts are chosen only where too few others are left
-        int live = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) live += v[i] > ninf ? 1 : 0;
-        whole = whole || __reduce_add_sync(0xffffffffu, live) < a.k;
     }
     // the k-th largest of the lanes' maxima (CPL of each lane)
     float top[CPL];
@@ -357,38 +394,56 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
             m += __popc(who);
         }
     }
-    whole = whole || m > 32 * CPL;
+    // more candidates than places; or fewer unmasked experts than k (the lanes
+    // then run out before k are seen, and every unmasked expert is a candidate)
+    const bool whole = m > 32 * CPL || m < a.k;   // decide the whole token in 64 bits
     int expert[CPL], rank[CPL];
     if (!whole) {
 #pragma unroll
         for (int q = 0; q < CPL; ++q)
             if (lane + 32 * q >= m) cv[lane + 32 * q] = ninf;
         __syncwarp();
-        float mine[CPL], tol[CPL];
-        bool close = false;
+        float mine[CPL];
 #pragma unroll
         for (int q = 0; q < CPL; ++q) {
             const int i = lane + 32 * q;
             mine[q] = cv[i];
             expert[q] = i < m ? ce[i] : 0;
             rank[q] = 0;
-            tol[q] = a.bias && i < m ? score_tol(a, mine[q]) : -1.0f;
         }
         for (int j = 0; j < m; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(cv + j);
-            const float o[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int q = 0; q < CPL; ++q) {
-                    const int i = lane + 32 * q;
-                    rank[q] += o[u] > mine[q] || (o[u] == mine[q] && j + u < i) ? 1 : 0;
-                    close |= j + u != i && fabsf(o[u] - mine[q]) <= tol[q];   // padding: inf or NaN
-                }
+            for (int q = 0; q < CPL; ++q)
+                rank[q] += (f.x > mine[q] ? 1 : 0) + (f.y > mine[q] ? 1 : 0) + (f.z > mine[q] ? 1 : 0) +
+                           (f.w > mine[q] ? 1 : 0);
         }
-        if (a.bias && __any_sync(0xffffffffu, close)) {
-            double* cd = reinterpret_cast<double*>(scratch + 2 * 32 * CPL);
-            rank_f64<CPL, LT>(a, l, ce, m, cd, rank);
+        // neighbours in the order: equal values share a rank and leave a hole
+        // (NaN) behind it
+        float* sorted = scratch + 2 * 32 * CPL;
+#pragma unroll
+        for (int q = 0; q < CPL; ++q) sorted[lane + 32 * q] = __int_as_float(0x7fffffff);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < CPL; ++q)
+            if (lane + 32 * q < m) sorted[rank[q]] = mine[q];
+        __syncwarp();
+        bool close = false;
+#pragma unroll
+        for (int q = 0; q < CPL; ++q)
+            if (lane + 32 * q < m && rank[q] + 1 < m)
+                close |= !(mine[q] - sorted[rank[q] + 1] > (a.bias ? score_tol(a, mine[q]) : 0.0f));
+        if (__any_sync(0xffffffffu, close)) {
+            if (a.bias) {
+                rank_f64<CPL, LT>(a, l, ce, m, reinterpret_cast<double*>(sorted), rank);
+            } else {
+                // equal logits: by position, which is expert order
+                for (int j = 0; j < m; ++j) {
+                    const float o = cv[j];
+#pragma unroll
+                    for (int q = 0; q < CPL; ++q) rank[q] += o == mine[q] && j < lane + 32 * q ? 1 : 0;
+                }
+            }
         }
 #pragma unroll
         for (int q = 0; q < CPL; ++q)
@@ -423,24 +478,18 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
         float sum = 0.0f;
 #pragma unroll
         for (int q = 0; q < CPL; ++q) {
-            u[q] = 0.0f;
-            if (on[q])
-                u[q] = !a.sigmoid ? expf(x[q] - big)
-                                  : __fdiv_rn(x[q] > 0.0f ? 1.0f : expf(x[q] - big), 1.0f + expf(x[q] > 0.0f ? -x[q] : x[q]));
+            u[q] = on[q] ? score_over(a, x[q], big) : 0.0f;
             sum += u[q];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = sum > 0.0f ? __frcp_rn(sum) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < CPL; ++q) u[q] = sum > 0.0f ? __fdiv_rn(u[q], sum) : 0.0f;
+        for (int q = 0; q < CPL; ++q) u[q] *= inv;
     } else {
 #pragma unroll
-        for (int q = 0; q < CPL; ++q) {
-            u[q] = 0.0f;
-            if (on[q])
-                u[q] = !a.sigmoid ? expf(x[q] - mx) * zinv
-                                  : __fdiv_rn(x[q] > 0.0f ? 1.0f : expf(x[q]), 1.0f + expf(x[q] > 0.0f ? -x[q] : x[q]));
-        }
+        for (int q = 0; q < CPL; ++q)
+            u[q] = !on[q] ? 0.0f : a.sigmoid ? score_over(a, x[q], 0.0f) : expf(x[q] - mx) * zinv;
     }
 #pragma unroll
     for (int q = 0; q < CPL; ++q)
@@ -455,7 +504,7 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
 constexpr int kScoreWarps = 4;
 
 template <int PER, int CPL, typename LT>
-__global__ void __launch_bounds__(32 * kScoreWarps) score_kernel(const ScoreArgs a) {
+__global__ void __launch_bounds__(32 * kScoreWarps, PER <= 8 ? 7 : 4) score_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) float scratch[];
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kScoreWarps + warp;
@@ -614,7 +663,7 @@ constexpr int kChunkWarps = 8;
 constexpr int kMaxChunks = 128;
 
 template <int PER, int CPL, typename LT>
-__global__ void __launch_bounds__(32 * kChunkWarps)
+__global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
     score_count_kernel(const ScoreArgs a, int32_t* chunk_hist, int* status, const int chunk_tokens,
                        const int C) {
     extern __shared__ __align__(16) float scratch[];
@@ -766,7 +815,7 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
     if (r && nchunks <= kMaxChunks && a.k >= 2) {
         static std::atomic<int> ready{-1};
         const size_t smem = kChunkWarps * sf + static_cast<size_t>(a.E) * sizeof(int);
-        const int C = a.k >= 8 ? 4 : 8;
+        const int C = 8;
         auto kern = score_count_kernel<PER, CPL, LT>;
         if (!smem_ready(kern, smem, ready)) return ST_CUDA;
         const int st = launch_cluster(kern, nchunks * C, 32 * kChunkWarps, C, smem, s, a, r->chunk_hist,
