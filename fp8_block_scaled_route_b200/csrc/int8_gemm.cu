@@ -35,7 +35,7 @@ constexpr int kKB = 128;             // K bytes per stage
 constexpr int kWRows = 128;          // weight rows per CTA tile
 constexpr int kWBytes = kWRows * kKB;
 constexpr int kGran = 16;            // gate / up rows of a granule
-constexpr int kWBox = 64;            // weight rows per TMA box
+constexpr int kWBox = 128;           // weight rows per TMA box
 constexpr int kMaxSplit = 8;         // CTAs of a cluster that share a K range
 
 struct I8Params {
@@ -210,7 +210,7 @@ template <int BT>
 struct Narrow {
     static constexpr int NST = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 3;
     static constexpr int STAGE = kWBytes + BT * kKB;
-    static constexpr int XBOX = BT < 32 ? BT : 32;   // token rows per TMA box
+    static constexpr int XBOX = BT < 64 ? BT : 64;   // token rows per TMA box
     static constexpr int COLS = 2 * BT < 32 ? 32 : 2 * BT;   // two accumulators
     // warps: 0 TMA, 1 MMA, then 4 epilogue warps, or 8 that share the columns
     static constexpr int PARTS = BT >= 32 ? 2 : 1;
@@ -222,11 +222,12 @@ struct Narrow {
 };
 
 // Weight boxes of a stage: lane i < w_boxes loads box i of the 128-row tile wt
-// of expert e.  Plain: two boxes of 64 rows.  Gated: two boxes of two granules
+// of expert e.  Plain: one box of 128 rows.  Gated: one box of four granules
 // (the map's dimensions are K, 16 rows, gate / up, granules, experts), or, when
-// granules would run over the end of a half, eight boxes of 16 rows.  Boxes of
-// 8 KB rather than 2 KB: with 2 KB boxes the copies' issue bounded the CTA-pair
-// kernel (K block of 128: ~1150 clocks against 512 of MMA).
+// granules would run over the end of a half, eight boxes of 16 rows.  Few large
+// boxes: the copies' issue bounded the CTA-pair kernel with 2 KB boxes (a K
+// block took ~1150 clocks against 512 of MMA; 8192^3 615 us) and still cost 8%
+// with 8 KB ones (381 us against 350).
 template <bool GATED>
 __device__ __forceinline__ int w_boxes(const I8Params& p) {
     return GATED && p.w_gran ? kWRows / kGran : kWRows / kWBox;
@@ -469,7 +470,7 @@ struct Pair {
     static constexpr int stages(int bt) {
         return RING / stage_bytes(bt) < MAX_NST ? RING / stage_bytes(bt) : MAX_NST;
     }
-    static constexpr int xbox(int bt) { return bt / 2 < 64 ? bt / 2 : 64; }   // token rows per TMA box
+    static constexpr int xbox(int bt) { return bt / 2; }   // token rows per TMA box
 };
 
 template <bool GATED, bool BF16>
@@ -572,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 
     if (warp == 0) {
         const int wb = w_boxes<GATED>(p);
-        const int xbox = min(p.bt >> 1, 64);          // token rows per box
+        const int xbox = p.bt >> 1;          // token rows per box
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
@@ -820,7 +821,7 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
         const long long units = static_cast<long long>(tiles) * z * std::min(g.E, g.R);
         while (S < kMaxSplit && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
     }
-    if (!make_map(&mx, g.a, g.R, g.K, bt < 32 ? bt : 32)) return ST_CUDA;
+    if (!make_map(&mx, g.a, g.R, g.K, bt < 64 ? bt : 64)) return ST_CUDA;
     switch (bt) {
         case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
         case 32: return launch_narrow<32, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
