@@ -254,17 +254,9 @@ __device__ __forceinline__ void load_weights(const I8Params& p, const CUtensorMa
 template <int BT, bool GATED, bool BF16>
 __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
     int8_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                       const I8Params p, const int S) {
+                       const I8Params p, int S) {
     using C = Narrow<BT>;
     extern __shared__ uint8_t smem_raw[];
-    const int e = blockIdx.y;
-    const int wt = S == 1 ? blockIdx.x : blockIdx.x / S;
-    const int ks = S == 1 ? 0 : blockIdx.x - wt * S;
-    int lo, hi;
-    expert_rows(p, e, lo, hi);
-    const int blocks = (hi - lo + BT - 1) / BT;
-    if (static_cast<int>(blockIdx.z) >= blocks) return;  // the whole cluster, if any
-
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     float* as_all = reinterpret_cast<float*>(base + C::NST * C::STAGE);
@@ -291,6 +283,15 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
     }
+    pdl_launch();
+    pdl_wait();
+    const int e = blockIdx.y;
+    const int wt = S == 1 ? blockIdx.x : blockIdx.x / S;
+    const int ks = S == 1 ? 0 : blockIdx.x - wt * S;
+    int lo, hi;
+    expert_rows(p, e, lo, hi);
+    const int blocks = (hi - lo + BT - 1) / BT;
+    if (static_cast<int>(blockIdx.z) >= blocks) return;  // the whole cluster, if any
     if (warp == 1) {
         tmem_alloc(tmem_s, C::COLS);
         tmem_relinquish();
@@ -513,6 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         tmem_relinquish_pair();
     }
     const int wtiles = GATED ? ((p.N >> 1) + 127) >> 7 : (p.N + 255) >> 8;   // of 256 weight rows
+    pdl_launch();
+    pdl_wait();
     if (warp == 2) {
         // first tile of every expert: a lane sums `per` experts, then a scan
         const int E = p.E;
@@ -768,19 +771,8 @@ int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& 
     static std::atomic<int> ready_dev{-1};
     auto kern = int8_narrow_kernel<BT, GATED, BF16>;
     if (!smem_ready(kern, C::SMEM, ready_dev)) return ST_CUDA;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(tiles * S, p.E, z);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = S;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+    return launch_dependent(kern, dim3(tiles * S, p.E, z), dim3(C::THREADS), S > 1 ? S : 0, C::SMEM, stream,
+                            mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <bool GATED, bool BF16>
@@ -789,8 +781,8 @@ int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p,
     static std::atomic<int> ready_dev{-1};
     auto kern = int8_pair_kernel<GATED, BF16>;
     if (!smem_ready(kern, Pair::SMEM, ready_dev)) return ST_CUDA;
-    kern<<<num_sms & ~1, Pair::THREADS, Pair::SMEM, stream>>>(mw, mx, p);
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+    return launch_dependent(kern, dim3(num_sms & ~1), dim3(Pair::THREADS), 0, Pair::SMEM, stream, mw, mx,
+                            p) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <bool GATED, bool BF16>

@@ -5,6 +5,31 @@
 
 namespace moe {
 
+// Launch of a kernel that calls pdl_wait (ptx.cuh): dependent launch, and a
+// cluster of `cluster` CTAs along x when above 0.
+template <typename... Args>
+inline cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, unsigned cluster,
+                                    size_t smem, cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cluster > 0) {
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = cluster;
+        at[1].val.clusterDim.y = 1;
+        at[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Epilogue of the grouped GEMM.
 enum Epilogue : int {
     EPI_BF16 = 0,          // plain: out[r, n] = bf16(G)

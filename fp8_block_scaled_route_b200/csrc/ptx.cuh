@@ -358,6 +358,19 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// ----------------------------------------------------------------- dependent launch
+// A kernel launched with the programmatic-serialization attribute may start
+// while its predecessor in the stream still runs.  pdl_wait returns when the
+// predecessor has finished and its writes are visible; every CTA calls it
+// before its first access to global memory (CTAs with nothing to do too: a
+// kernel that ended without waiting would let its own successor start before
+// its predecessor is done).  pdl_launch lets the successor's CTAs come in as
+// this kernel's leave room.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
     uint32_t r;
