@@ -36,6 +36,7 @@ constexpr int kWRows = 128;          // weight rows per CTA tile
 constexpr int kWBytes = kWRows * kKB;
 constexpr int kGran = 16;            // gate / up rows of a granule
 constexpr int kWBox = 128;           // weight rows per TMA box
+constexpr int MAX_E = kMaxRouteExperts;
 constexpr int kMaxSplit = 8;         // CTAs of a cluster that share a K range
 
 struct I8Params {
@@ -44,6 +45,7 @@ struct I8Params {
     const int32_t* m_indptr;
     void* out;
     int R, N, K, E, nkb;
+    int wtiles;   // narrow kernel: weight tiles of an expert
     int bt;       // pair kernel: token rows of a tile (64, 128 or 256)
     int nst;      // pair kernel: stages
     int w_gran;   // gated with N / 2 not a multiple of 16: weight boxes of one half granule
@@ -202,10 +204,71 @@ __device__ __forceinline__ void emit(const I8Params& p, const int (&s)[NC], cons
     }
 }
 
+// First work item of every expert (start[0..E], start[E] = their number) for
+// token blocks of bt rows and `wtiles` weight tiles, by one warp: a lane sums
+// the items of its experts, then a scan.
+__device__ __forceinline__ void item_table(const I8Params& p, int bt, int wtiles, int* start) {
+    const int lane = threadIdx.x & 31;
+    const int per = (p.E + 31) >> 5;
+    const int e0 = min(p.E, lane * per), e1 = min(p.E, e0 + per);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) {
+        int lo, hi;
+        expert_rows(p, e, lo, hi);
+        start[e] = (hi - lo + bt - 1) / bt * wtiles;   // items, replaced below
+        sum += start[e];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int e = e0; e < e1; ++e) {
+        const int n = start[e];
+        start[e] = run;
+        run += n;
+    }
+    if (lane == 31) start[p.E] = incl;
+}
+
+// Weight tile wt and token rows [row0, row0 + rows) of expert e.
+struct Item {
+    int e, wt, row0, rows;
+};
+
+// Item i of the table: token blocks inner, so that items that run side by side
+// share weight tiles.
+__device__ __forceinline__ Item item_of(const I8Params& p, int bt, const int* start, int i) {
+    int lo = 0, hi = p.E;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= i) lo = mid; else hi = mid;
+    }
+    int r0, r1;
+    expert_rows(p, lo, r0, r1);
+    const int local = i - start[lo];
+    const int blocks = (r1 - r0 + bt - 1) / bt;
+    Item x;
+    x.e = lo;
+    x.wt = local / blocks;
+    x.row0 = r0 + (local - x.wt * blocks) * bt;
+    x.rows = min(bt, r1 - x.row0);
+    return x;
+}
+
 // ------------------------------------------------------------ narrow kernel
-// One CTA per (128 weight rows, expert, token block stride z): for each of its
-// blocks of up to BT token rows, the whole K range (or, with a cluster of S
-// CTAs, the S-th part of it) streams through a ring of NST stages.
+// Tiles of 128 weight rows x up to BT token rows, two CTAs an SM, each with a
+// ring of NST stages.
+//  SPLIT = false: CTAs walk over the item table, the next items' loads running
+//    under an item's epilogue (4096 rows of 128 experts 1536 x 2048 gated: one
+//    CTA per tile 73 us, walking 69.5; and a crowded expert's token blocks are
+//    items of their own, where a CTA that looped over them took up to twice as
+//    long as the rest).
+//  SPLIT = true: few tiles and at most BT rows in all; a cluster of S CTAs
+//    shares a tile (grid S * weight tiles, experts), each with the S-th part of
+//    the K range.
 template <int BT>
 struct Narrow {
     static constexpr int NST = BT <= 16 ? 6 : BT <= 32 ? 5 : BT <= 64 ? 4 : 3;
@@ -218,7 +281,7 @@ struct Narrow {
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int PCOLS = BT / PARTS;         // columns of a warp
     static constexpr int AS = EPI_WARPS * PCOLS * 4; // row scales, PCOLS per epilogue warp
-    static constexpr int SMEM = 1024 + NST * STAGE + AS + 256;
+    static constexpr int SMEM = 1024 + NST * STAGE + AS + 256;   // and the item table, (E + 1) ints
 };
 
 // Weight boxes of a stage: lane i < w_boxes loads box i of the 128-row tile wt
@@ -251,7 +314,7 @@ __device__ __forceinline__ void load_weights(const I8Params& p, const CUtensorMa
     }
 }
 
-template <int BT, bool GATED, bool BF16>
+template <int BT, bool GATED, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
     int8_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                        const I8Params p, int S) {
@@ -283,15 +346,24 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX);
     }
+    int* start = reinterpret_cast<int*>(base + C::NST * C::STAGE + C::AS + 256);
     pdl_launch();
     pdl_wait();
-    const int e = blockIdx.y;
-    const int wt = S == 1 ? blockIdx.x : blockIdx.x / S;
-    const int ks = S == 1 ? 0 : blockIdx.x - wt * S;
-    int lo, hi;
-    expert_rows(p, e, lo, hi);
-    const int blocks = (hi - lo + BT - 1) / BT;
-    if (static_cast<int>(blockIdx.z) >= blocks) return;  // the whole cluster, if any
+    // SPLIT: the CTA's only item and its part of the K range
+    Item own{};
+    int ks = 0;
+    if constexpr (SPLIT) {
+        own.wt = blockIdx.x / S;
+        own.e = blockIdx.y;
+        ks = blockIdx.x - own.wt * S;
+        int r0, r1;
+        expert_rows(p, own.e, r0, r1);
+        own.row0 = r0;
+        own.rows = min(BT, r1 - own.row0);
+        if (own.rows <= 0) return;           // the whole cluster
+    } else if (warp == 2) {
+        item_table(p, BT, p.wtiles, start);
+    }
     if (warp == 1) {
         tmem_alloc(tmem_s, C::COLS);
         tmem_relinquish();
@@ -301,17 +373,19 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
     const WaitCtl wc{abort_s, p.status, p.timeout_ns};
-    const int kb0 = static_cast<int>(static_cast<long long>(p.nkb) * ks / S);
-    const int kb1 = static_cast<int>(static_cast<long long>(p.nkb) * (ks + 1) / S);
+    const int kb0 = SPLIT ? static_cast<int>(static_cast<long long>(p.nkb) * ks / S) : 0;
+    const int kb1 = SPLIT ? static_cast<int>(static_cast<long long>(p.nkb) * (ks + 1) / S) : p.nkb;
+    const int items = SPLIT ? 1 : start[p.E];
+    const int first = SPLIT ? 0 : blockIdx.x, step = SPLIT ? 1 : gridDim.x;
 
     if (warp == 0) {
         // lanes 0..7: weight boxes, lanes 8..: token boxes
         const int wb = w_boxes<GATED>(p);
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z) {
-            const int row0 = lo + tb * BT;
-            const int boxes = (min(BT, hi - row0) + C::XBOX - 1) / C::XBOX;
+        for (int i = first; i < items && ok; i += step) {
+            const Item x = SPLIT ? own : item_of(p, BT, start, i);
+            const int boxes = (x.rows + C::XBOX - 1) / C::XBOX;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
                 uint8_t* st = base + stage * C::STAGE;
@@ -319,10 +393,10 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
                     mbar_arrive_expect_tx(&full[stage], kWBytes + boxes * C::XBOX * kKB);
                 __syncwarp();
                 if (lane < wb)
-                    load_weights<GATED, false>(p, &tmW, st, &full[stage], kb, e, wt, lane);
+                    load_weights<GATED, false>(p, &tmW, st, &full[stage], kb, x.e, x.wt, lane);
                 else if (lane >= 8 && lane < 8 + boxes)
                     tma_load_2d(st + kWBytes + (lane - 8) * C::XBOX * kKB, &tmX, &full[stage], kb * kKB,
-                                row0 + (lane - 8) * C::XBOX);
+                                x.row0 + (lane - 8) * C::XBOX);
                 __syncwarp();
                 armed |= 1u << stage;
                 armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
@@ -335,9 +409,9 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
     } else if (warp == 1) {
         uint32_t stage = 0, phase = 0, it = 0;
         bool ok = true;
-        for (int tb = blockIdx.z; tb < blocks && ok; tb += gridDim.z, ++it) {
-            const int rows = min(BT, hi - (lo + tb * BT));
-            const uint32_t idesc = idesc_s8_s32(kWRows, (rows + 15) & ~15);
+        for (int i = first; i < items && ok; i += step, ++it) {
+            const Item x = SPLIT ? own : item_of(p, BT, start, i);
+            const uint32_t idesc = idesc_s8_s32(kWRows, (x.rows + 15) & ~15);
             const uint32_t acc = tmem + (it & 1) * BT;
             if (!warp_wait_spin(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
             tc_fence_after();
@@ -367,16 +441,17 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
         const int c0 = (warp - 2) / 4 * C::PCOLS;    // this warp's columns of a block
         float* as = as_all + (warp - 2) * C::PCOLS;
-        const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
         uint32_t it = 0;
-        for (int tb = blockIdx.z; tb < blocks; tb += gridDim.z, ++it) {
-            const int row0 = lo + tb * BT + c0;
+        for (int i = first; i < items; i += step, ++it) {
+            const Item x = SPLIT ? own : item_of(p, BT, start, i);
+            const LaneCol lc = lane_col<GATED>(p, x.e, x.wt, pos);
+            const int row0 = x.row0 + c0, hi = x.row0 + x.rows;
             const int nt = min(C::PCOLS, hi - row0);     // may be none
             stage_row_scales(p, as, row0, C::PCOLS, hi);
             if (!warp_wait(&tfull[it & 1], (it >> 1) & 1, wc, 6)) break;
             tc_fence_after();
             const uint32_t acc = lane_addr + (it & 1) * BT + c0;
-            if (S == 1) {
+            if constexpr (!SPLIT) {
                 for (int c = 0; c < nt; c += 16) {
                     uint32_t v[16];
                     tmem_ld16_async(acc + c, v);
@@ -403,7 +478,7 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
             }
         }
     }
-    if (S > 1) {
+    if constexpr (SPLIT) {
         // every thread of the cluster: partial sums visible; then the pair
         // columns (2 i, 2 i + 1) are added up and written, i mod S by CTA, then
         // in turn by the CTA's groups of four epilogue warps
@@ -411,11 +486,9 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
         cluster_sync_all();
         if (warp >= 2 && !*abort_s) {
             const int pos = (warp & 3) * 32 + lane;
-            const int row0 = lo + static_cast<int>(blockIdx.z) * BT;
-            const int nt = min(BT, hi - row0);
             const uint32_t mine = smem_u32(base) + pos * 4;
-            const LaneCol lc = lane_col<GATED>(p, e, wt, pos);
-            for (int c = 2 * (ks + S * ((warp - 2) / 4)); c < nt; c += 2 * S * C::PARTS) {
+            const LaneCol lc = lane_col<GATED>(p, own.e, own.wt, pos);
+            for (int c = 2 * (ks + S * ((warp - 2) / 4)); c < own.rows; c += 2 * S * C::PARTS) {
                 int t[kMaxSplit][2];     // every load in flight before the sums
 #pragma unroll
                 for (int r = 0; r < kMaxSplit; ++r) {
@@ -434,7 +507,7 @@ __global__ void __launch_bounds__(Narrow<BT>::THREADS, 2)
                 }
                 // column c's scales are in the buffer of the warp of its part and lanes
                 const float* as = as_all + ((c / C::PCOLS) * 4 + ((warp - 2) & 3)) * C::PCOLS + c % C::PCOLS;
-                emit<GATED, BF16, 2>(p, s, lc, as, row0 + c, hi);
+                emit<GATED, BF16, 2>(p, s, lc, as, own.row0 + c, own.row0 + own.rows);
             }
         }
         __syncwarp();
@@ -462,7 +535,6 @@ struct Pair {
     static constexpr int RING = 6 * (kWBytes + BT / 2 * kKB);
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-    static constexpr int MAX_E = 1024;
     static constexpr int AS = EPI_WARPS * 128 * 4;   // row scales, 128 per epilogue warp
     static constexpr int TABLE = ((MAX_E + 1) * 4 + 15) / 16 * 16;
     static constexpr int SMEM = 1024 + RING + AS + TABLE + 256;
@@ -516,32 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     const int wtiles = GATED ? ((p.N >> 1) + 127) >> 7 : (p.N + 255) >> 8;   // of 256 weight rows
     pdl_launch();
     pdl_wait();
-    if (warp == 2) {
-        // first tile of every expert: a lane sums `per` experts, then a scan
-        const int E = p.E;
-        const int per = (E + 31) >> 5;
-        const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
-        int sum = 0;
-        for (int e = e0; e < e1; ++e) {
-            int lo, hi;
-            expert_rows(p, e, lo, hi);
-            tstart[e] = hi - lo;         // rows, replaced below
-            sum += ((hi - lo + p.bt - 1) / p.bt) * wtiles;
-        }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        int run = incl - sum;
-        for (int e = e0; e < e1; ++e) {
-            const int n = (tstart[e] + p.bt - 1) / p.bt * wtiles;
-            tstart[e] = run;
-            run += n;
-        }
-        if (lane == 31) tstart[E] = incl;
-    }
+    if (warp == 2) item_table(p, p.bt, wtiles, tstart);
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();    // the peer's barriers and tensor memory are ready
@@ -551,26 +598,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     const int total = tstart[p.E];
     const int stride = gridDim.x >> 1;
 
-    struct Tile {
-        int e, wt, row0, rows;
-    };
-    // token blocks inner, so that concurrent pairs share weight tiles
+    // this CTA's half of tile t
     auto decode = [&](int t) {
-        int lo = 0, hi = p.E;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (tstart[mid] <= t) lo = mid; else hi = mid;
-        }
-        int r0, r1;
-        expert_rows(p, lo, r0, r1);
-        const int local = t - tstart[lo];
-        const int blocks = (r1 - r0 + p.bt - 1) / p.bt;
-        const int w = local / blocks;
-        Tile x;
-        x.e = lo;
-        x.wt = 2 * w + static_cast<int>(rank);
-        x.row0 = r0 + (local - w * blocks) * p.bt;
-        x.rows = min(p.bt, r1 - x.row0);
+        Item x = item_of(p, p.bt, tstart, t);
+        x.wt = 2 * x.wt + static_cast<int>(rank);
         return x;
     };
 
@@ -580,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
         for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
-            const Tile x = decode(t);
+            const Item x = decode(t);
             const int half = ((x.rows + 31) & ~31) >> 1;      // token rows of this CTA
             const int boxes = (half + xbox - 1) / xbox;
             const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * xbox;
@@ -616,7 +647,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
             uint32_t stage = 0, phase = 0, it = 0;
             bool ok = true;
             for (int t = blockIdx.x >> 1; t < total && ok; t += stride, ++it) {
-                const Tile x = decode(t);
+                const Item x = decode(t);
                 const uint32_t idesc = idesc_s8_s32(2 * kWRows, (x.rows + 31) & ~31);
                 const uint32_t acc = tmem + (it & 1) * C::BT;
                 if (!warp_wait_spin(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
@@ -651,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         float* as = as_all + (warp - 2) * 128;
         uint32_t it = 0;
         for (int t = blockIdx.x >> 1; t < total; t += stride, ++it) {
-            const Tile x = decode(t);
+            const Item x = decode(t);
             const int hi = x.row0 + x.rows;
             const int c0 = part * 128, end = min(x.rows, c0 + 128);
             const LaneCol lc = lane_col<GATED>(p, x.e, x.wt, pos);
@@ -765,14 +796,26 @@ int pair_tile(const I8GemmArgs& g, int per, int tiles) {
 }
 
 template <int BT, bool GATED, bool BF16>
-int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int tiles, int S,
-                  int z, cudaStream_t stream) {
+int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int S,
+                  int num_sms, cudaStream_t stream) {
     using C = Narrow<BT>;
+    const size_t smem = C::SMEM + (S > 1 ? 0 : (p.E + 1) * sizeof(int));
+    const int most = C::SMEM + (MAX_E + 1) * static_cast<int>(sizeof(int));
+    if (S > 1) {
+        static std::atomic<int> ready_dev{-1};
+        auto kern = int8_narrow_kernel<BT, GATED, BF16, true>;
+        if (!smem_ready(kern, most, ready_dev)) return ST_CUDA;
+        return launch_dependent(kern, dim3(p.wtiles * S, p.E), dim3(C::THREADS), S, smem, stream, mw, mx, p,
+                                S) == cudaSuccess ? ST_OK : ST_CUDA;
+    }
     static std::atomic<int> ready_dev{-1};
-    auto kern = int8_narrow_kernel<BT, GATED, BF16>;
-    if (!smem_ready(kern, C::SMEM, ready_dev)) return ST_CUDA;
-    return launch_dependent(kern, dim3(tiles * S, p.E, z), dim3(C::THREADS), S > 1 ? S : 0, C::SMEM, stream,
-                            mw, mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+    auto kern = int8_narrow_kernel<BT, GATED, BF16, false>;
+    if (!smem_ready(kern, most, ready_dev)) return ST_CUDA;
+    // at most as many items as this (one block more an expert than the rows fill)
+    const long long items = static_cast<long long>(p.wtiles) * (p.R / BT + std::min(p.E, p.R));
+    const unsigned grid = static_cast<unsigned>(std::min<long long>(items, 2 * num_sms));
+    return launch_dependent(kern, dim3(grid), dim3(C::THREADS), 0, smem, stream, mw, mx, p, 1) == cudaSuccess
+               ? ST_OK : ST_CUDA;
 }
 
 template <bool GATED, bool BF16>
@@ -789,7 +832,7 @@ template <bool GATED, bool BF16>
 int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int nkb = (g.K + kKB - 1) / kKB;
     const int w_gran = GATED && (g.N / 2) % kGran ? 1 : 0;
-    I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, 0, 0, w_gran,
+    I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, weight_tiles(g), 0, 0, w_gran,
                      g.status, g.timeout_ns};
     CUtensorMap mw, mx;
     if (GATED && !w_gran ? !make_gated_map(&mw, g.b, g.E, g.N, g.K)
@@ -806,19 +849,18 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     // rows of one expert of a balanced routing, with three standard deviations
     const int want = g.E == 1 ? g.R : std::min(g.R, per + static_cast<int>(3.0f * sqrtf(per)));
     const int bt = want <= 16 ? 16 : want <= 32 ? 32 : want <= 64 ? 64 : 128;
-    const int z = g.E == 1 ? (g.R + bt - 1) / bt : 1;
     // split K where the weight tiles leave SMs idle and an expert's rows are one block
     int S = 1;
-    if (g.E == 1 || g.R <= bt) {
-        const long long units = static_cast<long long>(tiles) * z * std::min(g.E, g.R);
+    if (g.R <= bt) {
+        const long long units = static_cast<long long>(tiles) * std::min(g.E, g.R);
         while (S < kMaxSplit && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
     }
     if (!make_map(&mx, g.a, g.R, g.K, bt < 64 ? bt : 64)) return ST_CUDA;
     switch (bt) {
-        case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
-        case 32: return launch_narrow<32, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
-        case 64: return launch_narrow<64, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
-        default: return launch_narrow<128, GATED, BF16>(mw, mx, p, tiles, S, z, stream);
+        case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, S, g.num_sms, stream);
+        case 32: return launch_narrow<32, GATED, BF16>(mw, mx, p, S, g.num_sms, stream);
+        case 64: return launch_narrow<64, GATED, BF16>(mw, mx, p, S, g.num_sms, stream);
+        default: return launch_narrow<128, GATED, BF16>(mw, mx, p, S, g.num_sms, stream);
     }
 }
 
