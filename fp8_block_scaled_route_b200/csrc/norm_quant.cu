@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 2 ? 512 : 1024, V == 2 && !W
     __shared__ double sums[32];
     __shared__ float red[32];
     __shared__ float rstd[8];
+    pdl_launch();
+    pdl_wait();
     const int TPR = blockDim.x;
     const int t = blockIdx.x * blockDim.y + threadIdx.y;
     const bool row_ok = t < p.T;
@@ -254,6 +256,8 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024)
                       float* __restrict__ q_scale) {
     // four groups a thread: 65536 x 2048 92 us with one, 68 with four
     __shared__ float red[32];
+    pdl_launch();
+    pdl_wait();
     const int TPR = blockDim.x;
     const int t = blockIdx.x * blockDim.y + threadIdx.y;
     const bool row_ok = t < T;
@@ -309,22 +313,20 @@ bool one_group(int T, int nvec, int num_sms) { return T <= num_sms && nvec > 32 
 template <bool WARP, int V>
 int launch_norm(const RmsNormArgs& p, dim3 block, cudaStream_t s) {
     const unsigned grid = (static_cast<unsigned>(p.T) + block.y - 1) / block.y;
-    switch (p.fmt) {
-        case NQ_NONE: rmsnorm_kernel<WARP, V, NQ_NONE><<<grid, block, 0, s>>>(p); break;
-        case NQ_FP8: rmsnorm_kernel<WARP, V, NQ_FP8><<<grid, block, 0, s>>>(p); break;
-        case NQ_MXFP8: rmsnorm_kernel<WARP, V, NQ_MXFP8><<<grid, block, 0, s>>>(p); break;
-        default: rmsnorm_kernel<WARP, V, NQ_INT8><<<grid, block, 0, s>>>(p); break;
-    }
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+    auto kern = p.fmt == NQ_NONE    ? rmsnorm_kernel<WARP, V, NQ_NONE>
+                : p.fmt == NQ_FP8   ? rmsnorm_kernel<WARP, V, NQ_FP8>
+                : p.fmt == NQ_MXFP8 ? rmsnorm_kernel<WARP, V, NQ_MXFP8>
+                                    : rmsnorm_kernel<WARP, V, NQ_INT8>;
+    return launch_dependent(kern, dim3(grid), block, 0, 0, s, p) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <bool WARP, int V>
 int launch_q8(const void* x, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
               float* q_scale, dim3 block, cudaStream_t s) {
     const unsigned grid = (static_cast<unsigned>(T) + block.y - 1) / block.y;
-    int8_quant_kernel<WARP, V><<<grid, block, 0, s>>>(static_cast<const __nv_bfloat16*>(x), T, K, k, R,
-                                                      inv_perm, q, q_scale);
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+    return launch_dependent(int8_quant_kernel<WARP, V>, dim3(grid), block, 0, 0, s,
+                            static_cast<const __nv_bfloat16*>(x), T, K, k, R, inv_perm, q, q_scale) ==
+                   cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 }  // namespace

@@ -508,6 +508,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, PER <= 8 ? 7 : 4) score_kern
     extern __shared__ __align__(16) float scratch[];
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kScoreWarps + warp;
+    pdl_launch();
+    pdl_wait();
     if (t >= a.T) return;
     score_token<PER, CPL, LT>(a, t, scratch + warp * scratch_floats<CPL>(a.E, a.n_group > 1), nullptr);
 }
@@ -518,18 +520,15 @@ __global__ void __launch_bounds__(32 * kScoreWarps, PER <= 8 ? 7 : 4) score_kern
 // ones of its segment (one ballot per expert-id bit gives the lanes with the
 // same expert); a thread per expert then scans the segments' counts.
 //   cnt   shared [NW][E], zeroed
-//   base  shared [E]: first output row of each expert (filled by `first_rows`
-//         from the experts' counts, which it gets for all E experts)
-constexpr int kSteps = 9;   // most 32-pair steps of a segment
-
-template <int NW>
+//   base  shared [E]: first output row of each expert
+template <int NW, int STEPS>   // warps, most 32-pair steps of a segment
 struct Segment {
-    int p0, n;             // this warp's pairs: p0 + [0, n)
-    int e[kSteps], r[kSteps];
+    int p0, n;                 // this warp's pairs: p0 + [0, n)
+    int e[STEPS], r[STEPS];    // each pair's expert and its rank in the segment
 };
 
-template <int NW>
-__device__ __forceinline__ void count_pairs(Segment<NW>& s, const int32_t* ids, int first, int n, int E,
+template <int NW, int kSteps>
+__device__ __forceinline__ void count_pairs(Segment<NW, kSteps>& s, const int32_t* ids, int first, int n, int E,
                                             int nbits, int* cnt) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per = ((n + NW - 1) / NW + 31) & ~31;
@@ -559,8 +558,8 @@ __device__ __forceinline__ void count_pairs(Segment<NW>& s, const int32_t* ids, 
     }
 }
 
-template <int NW>
-__device__ __forceinline__ void place_pairs(const Segment<NW>& s, int E, const int* cnt, const int* base,
+template <int NW, int kSteps>
+__device__ __forceinline__ void place_pairs(const Segment<NW, kSteps>& s, int E, const int* cnt, const int* base,
                                             int32_t* perm, int32_t* inv_perm) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -603,12 +602,13 @@ __host__ __device__ inline int bits_of(int E) {
 constexpr int kSmallWarps = 16;
 constexpr int kSmallCluster = 8;
 constexpr int kSmallTokens = 256;
-constexpr int kSmallPairs = kSmallWarps * kSteps * 32;
+constexpr int kSmallSteps = 9;
+constexpr int kSmallPairs = kSmallWarps * kSmallSteps * 32;
 
 template <int PER, int CPL, typename LT>
 __global__ void __launch_bounds__(32 * kSmallWarps)
     score_route_small(const ScoreArgs a, int32_t* m_indptr, int32_t* perm, int32_t* inv_perm,
-                      int* status, const int nbits) {
+                      int* status, int nbits) {
     extern __shared__ __align__(16) float scratch[];
     __shared__ int warp_tot[kSmallWarps];
     const int warp = threadIdx.x >> 5;
@@ -616,6 +616,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
     const int sf = scratch_floats<CPL>(a.E, a.n_group > 1);
     int* cnt = reinterpret_cast<int*>(scratch + kSmallWarps * sf);   // [warps][E]
     int* base = cnt + kSmallWarps * a.E;                             // [E]
+    pdl_launch();
+    pdl_wait();
     if (rank == 0) {
         for (int i = threadIdx.x; i < kSmallWarps * a.E; i += 32 * kSmallWarps) cnt[i] = 0;
         if (threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
     cluster_sync_all();      // every CTA's ids are visible
     if (rank != 0) return;
     const int R = a.T * a.k;
-    Segment<kSmallWarps> seg;
+    Segment<kSmallWarps, kSmallSteps> seg;
     count_pairs(seg, a.ids, 0, R, a.E, nbits, cnt);
     __syncthreads();
     // experts [e0, e1) of this thread: counts of the segments before, totals
@@ -664,13 +666,13 @@ constexpr int kMaxChunks = 128;
 
 template <int PER, int CPL, typename LT>
 __global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
-    score_count_kernel(const ScoreArgs a, int32_t* chunk_hist, int* status, const int chunk_tokens,
-                       const int C) {
+    score_count_kernel(const ScoreArgs a, int32_t* chunk_hist, int* status, int chunk_tokens, int C) {
     extern __shared__ __align__(16) float scratch[];
     const int warp = threadIdx.x >> 5;
     const int sf = scratch_floats<CPL>(a.E, a.n_group > 1);
     int* hist = reinterpret_cast<int*>(scratch + kChunkWarps * sf);
     const int chunk = blockIdx.x / C, rank = blockIdx.x - chunk * C;
+    pdl_wait();
     for (int e = threadIdx.x; e < a.E; e += 32 * kChunkWarps) hist[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
     __syncthreads();
@@ -679,6 +681,7 @@ __global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
         score_token<PER, CPL, LT>(a, t, scratch + warp * sf, hist);
     __syncwarp();
     cluster_sync_all();
+    pdl_launch();            // not before: the successor's CTAs would take this kernel's places
     for (int e = rank * 32 * kChunkWarps + threadIdx.x; e < a.E; e += C * 32 * kChunkWarps) {
         int n = 0;
         for (int r = 0; r < C; ++r) n += ld_shared_cluster_s32(mapa_shared(smem_u32(hist + e), r));
@@ -690,60 +693,62 @@ __global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
 
 // Second launch: one CTA per chunk adds up the counts of the chunks before it
 // (every CTA for itself: at most 128 rows of counts out of L2) and places its
-// pairs.
-template <int EPT>
-__global__ void __launch_bounds__(32 * kChunkWarps)
+// pairs.  Thread (g, e) of the 1024 reads every G-th row of counts at expert e,
+// so that 64 chunks of 256 experts are one round of 16 loads a thread; 32 warps
+// have one or two steps of 32 pairs each.
+constexpr int kPlaceWarps = 32;
+
+__global__ void __launch_bounds__(32 * kPlaceWarps)
     place_kernel(const int32_t* __restrict__ ids, int R, int E, int nbits, int chunk_pairs,
                  const int32_t* __restrict__ chunk_hist, int32_t* m_indptr, int32_t* perm,
                  int32_t* inv_perm) {
     extern __shared__ __align__(16) int smem[];
-    __shared__ int warp_tot[kChunkWarps];
+    __shared__ int warp_tot[kPlaceWarps];
+    __shared__ int part_total[32 * kPlaceWarps], part_before[32 * kPlaceWarps];
     int* cnt = smem;                       // [warps][E]
-    int* base = cnt + kChunkWarps * E;     // [E]
+    int* base = cnt + kPlaceWarps * E;     // [E]
     const int nchunks = gridDim.x, chunk = blockIdx.x;
-    for (int i = threadIdx.x; i < kChunkWarps * E; i += 32 * kChunkWarps) cnt[i] = 0;
+    const int e = threadIdx.x & ((1 << nbits) - 1), g = threadIdx.x >> nbits;   // E <= 2^nbits <= 1024
+    const int G = (32 * kPlaceWarps) >> nbits;
+    pdl_wait();
+    int total = 0, before = 0;
+    for (int c0 = g; c0 < nchunks; c0 += 16 * G) {
+        int h[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int c = c0 + i * G;
+            h[i] = c < nchunks && e < E ? __ldcg(chunk_hist + static_cast<long long>(c) * E + e) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (c0 + i * G < chunk) before += h[i];
+            total += h[i];
+        }
+    }
+    part_total[threadIdx.x] = total;
+    part_before[threadIdx.x] = before;
+    for (int i = threadIdx.x; i < kPlaceWarps * E; i += 32 * kPlaceWarps) cnt[i] = 0;
     __syncthreads();
     const int first = chunk * chunk_pairs;
-    Segment<kChunkWarps> seg;
+    Segment<kPlaceWarps, 2> seg;
     count_pairs(seg, ids, first, min(chunk_pairs, R - first), E, nbits, cnt);
-    // experts EPT * thread + i: pairs in all chunks and in the chunks before
-    const int e0 = threadIdx.x * EPT;
-    int total[EPT] = {}, before[EPT] = {};
-    for (int c0 = 0; c0 < nchunks; c0 += 16) {
-        int h[16][EPT];
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int i = 0; i < EPT; ++i)
-                h[c][i] = c0 + c < nchunks && e0 + i < E
-                              ? chunk_hist[static_cast<long long>(c0 + c) * E + e0 + i] : 0;
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                if (c0 + c < chunk) before[i] += h[c][i];
-                total[i] += h[c][i];
-            }
-    }
-    int sum = 0;
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) sum += total[i];
-    __syncthreads();                       // every warp's counts are in cnt
-    int row = cta_exclusive<kChunkWarps>(sum, warp_tot);
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-        const int e = e0 + i;
-        if (e < E) {
-            base[e] = row + before[i];
-            if (chunk == 0) m_indptr[e] = row;
-            row += total[i];
-            int run = 0;
-#pragma unroll
-            for (int w = 0; w < kChunkWarps; ++w) {
-                const int n = cnt[w * E + e];
-                cnt[w * E + e] = run;
-                run += n;
-            }
+    const bool mine = threadIdx.x < E;     // one thread an expert from here
+    total = before = 0;
+    if (mine)
+        for (int i = 0; i < G; ++i) {
+            total += part_total[(i << nbits) + e];
+            before += part_before[(i << nbits) + e];
+        }
+    const int row = cta_exclusive<kPlaceWarps>(total, warp_tot);   // a barrier: cnt is complete
+    if (mine) {
+        base[e] = row + before;
+        if (chunk == 0) m_indptr[e] = row;
+        int run = 0;
+#pragma unroll 16
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            const int n = cnt[w * E + e];
+            cnt[w * E + e] = run;
+            run += n;
         }
     }
     if (chunk == 0 && threadIdx.x == 0) m_indptr[E] = R;
@@ -756,7 +761,7 @@ __global__ void __launch_bounds__(32 * kChunkWarps)
 // kernel; `ready_dev` is the kernel's own (alternating devices set it again).
 template <typename Kern>
 bool smem_ready(Kern kern, size_t bytes, std::atomic<int>& ready_dev) {
-    if (bytes <= 48 * 1024) return true;
+    if (bytes <= 32 * 1024) return true;   // with the static part below the 48 KB that need none
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (ready_dev.load() == dev) return true;
@@ -766,34 +771,14 @@ bool smem_ready(Kern kern, size_t bytes, std::atomic<int>& ready_dev) {
     return true;
 }
 
-template <typename... Args>
-int launch_cluster(void (*kern)(Args...), unsigned grid, unsigned block, unsigned cluster, size_t smem,
-                   cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? ST_OK : ST_CUDA;
-}
-
 int launch_place(const RouteArgs& r, int chunk_pairs, int nchunks, cudaStream_t s) {
-    const size_t smem = static_cast<size_t>(kChunkWarps + 1) * r.E * sizeof(int);
-    const int R = r.T * r.k, nb = bits_of(r.E);
-    if (r.E <= 32 * kChunkWarps)
-        place_kernel<1><<<nchunks, 32 * kChunkWarps, smem, s>>>(r.topk_ids, R, r.E, nb, chunk_pairs,
-                                                                r.chunk_hist, r.m_indptr, r.perm, r.inv_perm);
-    else
-        place_kernel<4><<<nchunks, 32 * kChunkWarps, smem, s>>>(r.topk_ids, R, r.E, nb, chunk_pairs,
-                                                                r.chunk_hist, r.m_indptr, r.perm, r.inv_perm);
-    return cudaGetLastError() == cudaSuccess ? ST_OK : ST_CUDA;
+    static std::atomic<int> ready{-1};
+    const size_t smem = (kPlaceWarps + 1ull) * r.E * sizeof(int);
+    if (!smem_ready(place_kernel, smem, ready)) return ST_CUDA;
+    return launch_dependent(place_kernel, dim3(nchunks), dim3(32 * kPlaceWarps), 0, smem, s, r.topk_ids,
+                            r.T * r.k, r.E, bits_of(r.E), chunk_pairs,
+                            static_cast<const int32_t*>(r.chunk_hist), r.m_indptr, r.perm, r.inv_perm) ==
+                   cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <int PER, int CPL, typename LT>
@@ -805,8 +790,9 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
         const size_t smem = kSmallWarps * sf + (kSmallWarps + 1ull) * a.E * sizeof(int);
         auto kern = score_route_small<PER, CPL, LT>;
         if (!smem_ready(kern, smem, ready)) return ST_CUDA;
-        return launch_cluster(kern, kSmallCluster, 32 * kSmallWarps, kSmallCluster, smem, s, a, r->m_indptr,
-                              r->perm, r->inv_perm, r->status, static_cast<const int>(bits_of(a.E)));
+        return launch_dependent(kern, dim3(kSmallCluster), dim3(32 * kSmallWarps), kSmallCluster, smem, s, a,
+                                r->m_indptr, r->perm, r->inv_perm, r->status, bits_of(a.E)) == cudaSuccess
+                   ? ST_OK : ST_CUDA;
     }
     // chunks of whole tokens, at least kRouteChunk pairs each, so that their
     // counts fit the workspace's
@@ -818,17 +804,18 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
         const int C = 8;
         auto kern = score_count_kernel<PER, CPL, LT>;
         if (!smem_ready(kern, smem, ready)) return ST_CUDA;
-        const int st = launch_cluster(kern, nchunks * C, 32 * kChunkWarps, C, smem, s, a, r->chunk_hist,
-                                      r->status, chunk_tokens, C);
-        return st ? st : launch_place(*r, chunk_tokens * a.k, nchunks, s);
+        if (launch_dependent(kern, dim3(nchunks * C), dim3(32 * kChunkWarps), C, smem, s, a, r->chunk_hist,
+                             r->status, chunk_tokens, C) != cudaSuccess)
+            return ST_CUDA;
+        return launch_place(*r, chunk_tokens * a.k, nchunks, s);
     }
     if (a.T > 0) {
         static std::atomic<int> ready{-1};
         auto kern = score_kernel<PER, CPL, LT>;
         if (!smem_ready(kern, kScoreWarps * sf, ready)) return ST_CUDA;
-        kern<<<static_cast<unsigned>((a.T + kScoreWarps - 1) / kScoreWarps), 32 * kScoreWarps,
-               kScoreWarps * sf, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return ST_CUDA;
+        const unsigned grid = static_cast<unsigned>((a.T + kScoreWarps - 1) / kScoreWarps);
+        if (launch_dependent(kern, dim3(grid), dim3(32 * kScoreWarps), 0, kScoreWarps * sf, s, a) != cudaSuccess)
+            return ST_CUDA;
     }
     if (!r) return ST_OK;
     RouteArgs rr = *r;

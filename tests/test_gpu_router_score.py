@@ -100,7 +100,7 @@ SHAPES = [  # T, E, k, n_group, topk_group, group_top
     (1, 1, 1, 1, 1, 1), (1, 256, 8, 8, 4, 2), (2, 5, 5, 1, 1, 1), (33, 60, 6, 5, 2, 1),
     (64, 256, 8, 8, 4, 2), (129, 128, 8, 1, 1, 1), (200, 160, 6, 8, 3, 1), (130, 1024, 32, 32, 32, 2),
     (37, 1000, 9, 4, 1, 2), (300, 512, 16, 16, 5, 2), (1030, 64, 8, 4, 2, 2), (40, 32, 3, 32, 4, 2),
-    (50, 257, 4, 1, 1, 1),
+    (50, 257, 4, 1, 1, 1), (700, 300, 8, 1, 1, 1), (1100, 372, 6, 4, 3, 2), (257, 700, 31, 7, 6, 1),
 ]
 
 
