@@ -73,6 +73,7 @@ const DevInfo* dev_info() {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Workspace of the fused layer, in carve order.
@@ -319,7 +320,7 @@ int moe_route_permute(const int32_t* topk_ids, int T, int k, int E, int32_t* m_i
 }
 
 // Argument rules of the scored router; MOE_OK or the error to return.
-static int check_score(const void* logits, int logits_dtype, int T, int E, int k, int scoring,
+static int check_score(const void* logits, int logits_dtype, const float* bias, int T, int E, int k, int scoring,
                        int n_group, int topk_group, int group_top, float scale, const void* ids,
                        const void* w) {
     if (T < 0 || E < 1 || k < 1 || k > E || k > MOE_ROUTER_MAX_K) return MOE_ERR_INVALID_ARG;
@@ -333,6 +334,7 @@ static int check_score(const void* logits, int logits_dtype, int T, int E, int k
     if (!(scale > 0.0f) || scale > 3.402823466e38f) return MOE_ERR_INVALID_ARG;
     if (static_cast<long long>(T) * k > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
     if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(logits) || !aligned4(bias) || !aligned4(ids) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 
@@ -340,7 +342,7 @@ int moe_router_score_topk(const void* logits, int logits_dtype, const float* bia
                           int k, int scoring, int n_group, int topk_group, int group_top,
                           int renorm, float scale, int32_t* topk_ids, float* topk_w,
                           moe_stream_t stream) {
-    if (int st = check_score(logits, logits_dtype, T, E, k, scoring, n_group, topk_group, group_top,
+    if (int st = check_score(logits, logits_dtype, bias, T, E, k, scoring, n_group, topk_group, group_top,
                              scale, topk_ids, topk_w))
         return st;
     const DevInfo* d = dev_info();
@@ -356,10 +358,11 @@ int moe_router_score_route(const void* logits, int logits_dtype, const float* bi
                            int renorm, float scale, int32_t* topk_ids, float* topk_w,
                            int32_t* m_indptr, int32_t* perm, int32_t* inv_perm, void* ws,
                            size_t ws_bytes, moe_stream_t stream) {
-    if (int st = check_score(logits, logits_dtype, T, E, k, scoring, n_group, topk_group, group_top,
+    if (int st = check_score(logits, logits_dtype, bias, T, E, k, scoring, n_group, topk_group, group_top,
                              scale, topk_ids, topk_w))
         return st;
     if (!m_indptr || !ws || (T > 0 && !perm)) return MOE_ERR_INVALID_ARG;
+    if (!aligned4(m_indptr) || !aligned4(perm) || !aligned4(inv_perm)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < route_ws_bytes(T, k, E) || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
@@ -387,7 +390,7 @@ int moe_rmsnorm_quant(const void* x, const void* residual, const void* weight, i
     if (T > 0 && (!x || !weight)) return MOE_ERR_INVALID_ARG;
     if (T > 0 && q_format != MOE_Q_NONE && (!q || !q_scale)) return MOE_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
-        !aligned16(y) || !aligned16(q) || (reinterpret_cast<uintptr_t>(q_scale) & 3))
+        !aligned16(y) || !aligned16(q) || !aligned4(q_scale))
         return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
@@ -402,7 +405,8 @@ int int8_quantize(const void* x, int T, int K, int k, int R, const int32_t* inv_
     if (!inv_perm && (k != 1 || R < T)) return MOE_ERR_INVALID_ARG;
     if (K > MOE_NORM_MAX_H) return MOE_ERR_UNSUPPORTED;
     if (T > 0 && (!x || (R > 0 && (!q || !q_scale)))) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned4(inv_perm) || !aligned4(q_scale))
+        return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
     return launch_int8_quant(x, T, K, k, R, inv_perm, q, q_scale, d->sms,
@@ -418,7 +422,9 @@ int int8_moe_gemm(const int8_t* a, const int8_t* b, const float* a_scale, const 
     if (E > MOE_MAX_EXPERTS || K > MOE_INT8_MAX_K) return MOE_ERR_UNSUPPORTED;
     if (static_cast<long long>(E) * N > 0x7ffffe00ll || R > 0x7ffffe00) return MOE_ERR_UNSUPPORTED;
     if (R > 0 && (!a || !b || !a_scale || !b_scale || !out)) return MOE_ERR_INVALID_ARG;
-    if (!aligned16(a) || !aligned16(b) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned4(a_scale) || !aligned4(b_scale) ||
+        !aligned4(m_indptr))
+        return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
     const I8GemmArgs g{a, b, a_scale, b_scale, m_indptr, out, out_dtype == MOE_DTYPE_BF16, R, N, K, E,

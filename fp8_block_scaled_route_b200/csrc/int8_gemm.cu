@@ -546,10 +546,15 @@ struct Pair {
     static constexpr int xbox(int bt) { return bt / 2; }   // token rows per TMA box
 };
 
-template <bool GATED, bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
+//
+// SPLIT: few tiles (one expert); a cluster of S pairs shares each, a pair summing
+// the S-th part of the K range.  Every CTA then lays its 128 weight rows' sums out
+// in shared memory and adds up, over the pairs, every S-th 16 columns of them.
+// 256 rows x 4096 x 7168: 19.3 us with one pair a tile, 15.6 with two.
+template <bool GATED, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(Pair::THREADS, 1)
     int8_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                     const I8Params p) {
+                     const I8Params p, int S) {
     using C = Pair;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>(
@@ -564,7 +569,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     uint32_t* tmem_s = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_s = reinterpret_cast<volatile int*>(tmem_s + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t crank = cluster_ctarank();
+    const uint32_t rank = crank & 1;                 // place in the pair
+    const int ks = SPLIT ? static_cast<int>(crank >> 1) : 0;
     const int nst = p.nst, stage_bytes = kWBytes + p.bt * (kKB / 2);
     if (threadIdx.x == 0) {
         for (int i = 0; i < nst; ++i) {
@@ -595,8 +602,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_s;
     const WaitCtl wc{abort_s, p.status, p.timeout_ns};
-    const int total = tstart[p.E];
-    const int stride = gridDim.x >> 1;
+    const int kb0 = SPLIT ? static_cast<int>(static_cast<long long>(p.nkb) * ks / S) : 0;
+    const int kb1 = SPLIT ? static_cast<int>(static_cast<long long>(p.nkb) * (ks + 1) / S) : p.nkb;
+    // SPLIT: the cluster's only tile (the grid has as many clusters as R rows make
+    // tiles; m_indptr may name fewer rows)
+    const int first = SPLIT ? blockIdx.x / (2 * S) : blockIdx.x >> 1;
+    const int total = SPLIT ? min(first + 1, tstart[p.E]) : tstart[p.E];
+    const int stride = SPLIT ? 1 : gridDim.x >> 1;
 
     // this CTA's half of tile t
     auto decode = [&](int t) {
@@ -610,12 +622,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         const int xbox = p.bt >> 1;          // token rows per box
         uint32_t stage = 0, phase = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        for (int t = blockIdx.x >> 1; t < total && ok; t += stride) {
+        for (int t = first; t < total && ok; t += stride) {
             const Item x = decode(t);
             const int half = ((x.rows + 31) & ~31) >> 1;      // token rows of this CTA
             const int boxes = (half + xbox - 1) / xbox;
             const int xrow = x.row0 + static_cast<int>(rank) * half + (lane - 8) * xbox;
-            for (int kb = 0; kb < p.nkb; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!warp_wait_spin(&empty[stage], phase ^ 1, wc, 1)) { ok = false; break; }
                 uint8_t* st = base + stage * stage_bytes;
                 if (rank == 0 && lane == 0)
@@ -644,15 +656,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0) {
+            const uint16_t both = static_cast<uint16_t>(3u << crank);   // this pair's CTAs
             uint32_t stage = 0, phase = 0, it = 0;
             bool ok = true;
-            for (int t = blockIdx.x >> 1; t < total && ok; t += stride, ++it) {
+            for (int t = first; t < total && ok; t += stride, ++it) {
                 const Item x = decode(t);
                 const uint32_t idesc = idesc_s8_s32(2 * kWRows, (x.rows + 31) & ~31);
                 const uint32_t acc = tmem + (it & 1) * C::BT;
                 if (!warp_wait_spin(&tempty[it & 1], ((it >> 1) & 1) ^ 1, wc, 3)) break;
                 tc_fence_after();
-                for (int kb = 0; kb < p.nkb; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!warp_wait_spin(&full[stage], phase, wc, 4)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t sw = smem_u32(base + stage * stage_bytes);
@@ -660,9 +673,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_i8_pair(acc, smem_desc_k_sw128(sw + kk * 32),
-                                         smem_desc_k_sw128(sw + kWBytes + kk * 32), idesc, kb > 0 || kk > 0);
-                        umma_commit_pair(&empty[stage]);
-                        if (kb == p.nkb - 1) umma_commit_pair(&tfull[it & 1]);
+                                         smem_desc_k_sw128(sw + kWBytes + kk * 32), idesc, kb > kb0 || kk > 0);
+                        umma_commit_pair(&empty[stage], both);
+                        if (kb == kb1 - 1) umma_commit_pair(&tfull[it & 1], both);
                     }
                     __syncwarp();
                     if (++stage == nst) { stage = 0; phase ^= 1; }
@@ -678,10 +691,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
         const int part = (warp - 2) >> 2;    // columns [128 part, 128 part + 128)
         const int pos = q * 32 + lane;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+        const uint32_t tempty0 = mapa_shared(smem_u32(tempty), crank & ~1u);
         float* as = as_all + (warp - 2) * 128;
         uint32_t it = 0;
-        for (int t = blockIdx.x >> 1; t < total; t += stride, ++it) {
+        for (int t = first; t < total; t += stride, ++it) {
             const Item x = decode(t);
             const int hi = x.row0 + x.rows;
             const int c0 = part * 128, end = min(x.rows, c0 + 128);
@@ -702,14 +715,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair::THREADS, 1)
                 int s[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) s[j] = static_cast<int>(v[j]);
-                emit<GATED, BF16, 32>(p, s, lc, as + (c - c0), x.row0 + c, hi);
+                if constexpr (!SPLIT) {
+                    emit<GATED, BF16, 32>(p, s, lc, as + (c - c0), x.row0 + c, hi);
+                } else {
+                    // the pipeline's stages are free: every MMA has completed
+                    int* part_sums = reinterpret_cast<int*>(base);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part_sums[(c + j) * kWRows + pos] = s[j];
+                }
             }
             if (end <= c0 && lane == 0) mbar_arrive_cluster(tempty0 + (it & 1) * 8);
         }
     }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_sync_all();    // every pair's sums are visible
+        if (warp >= 2 && first < total && !*abort_s) {
+            const Item x = decode(first);
+            const int pos = (warp & 3) * 32 + lane;
+            const LaneCol lc = lane_col<GATED>(p, x.e, x.wt, pos);
+            const uint32_t mine = smem_u32(base) + pos * 4;
+            // 16 columns at a time: chunk i by pair i mod S, then in turn by the
+            // CTA's two groups of four warps
+            for (int c = 16 * (ks + S * ((warp - 2) >> 2)); c < x.rows; c += 32 * S) {
+                int s[16] = {};
+                for (int r = 0; r < S; ++r) {
+                    const uint32_t at = mapa_shared(mine, 2 * r + rank) + c * kWRows * 4;
+                    int v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = ld_shared_cluster_s32(at + j * kWRows * 4);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] += v[j];
+                }
+                // the scales of column c are in its part's buffers
+                const float* as = as_all + ((c >> 7) * 4 + ((warp - 2) & 3)) * 128 + (c & 127);
+                emit<GATED, BF16, 16>(p, s, lc, as, x.row0 + c, x.row0 + x.rows);
+            }
+        }
+    }
     tc_fence_before();
     __syncwarp();
-    cluster_sync_all();    // both CTAs done with barriers, operands and tensor memory
+    cluster_sync_all();    // all CTAs done with barriers, operands and tensor memory
     tc_fence_after();
     if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
@@ -773,23 +819,65 @@ int weight_tiles(const I8GemmArgs& g) {
     return g.gated ? (g.N / 2 + 63) / 64 : (g.N + 127) / 128;
 }
 
-// Token rows of a pair tile: the fewest clocks for a balanced routing.  A
-// 128-byte K block costs an SM its loads, 16 KB of weights and 64 bytes a token
-// row at ~58 B/clk (measured), or 2 clocks of MMA a token row; a tile adds ~3000
-// clocks of pipeline fill and epilogue.  Smaller tiles pay where 256-row ones
-// leave pairs idle: 256 rows x 4096 x 7168: tiles of 256 rows 24.5 us, of 64
-// rows 21.8 us.
-int pair_tile(const I8GemmArgs& g, int per, int tiles) {
+// Token rows of a pair tile and pairs that share one: the fewest clocks for a
+// balanced routing.  A 128-byte K block costs an SM its loads, 16 KB of weights
+// and 64 bytes a token row at ~58 B/clk (measured), or 2 clocks of MMA a token
+// row; a tile adds ~3000 clocks of pipeline fill and epilogue, a split one ~2000
+// and 16 a token row for laying out and exchanging its sums.  Only the tiles of
+// one expert are split (their number has to be known here), and only where
+// their clusters all run side by side (B200: 33 of 4 CTAs, 15 of 8; 16 of 8 took
+// a second round, 31 us where 19 would do).
+struct PairPlan {
+    int bt, S;
+};
+
+// Clusters of `ctas` CTAs of the split pair kernel that the current device runs
+// at once; asked once per device.
+int pair_clusters(int ctas) {
+    static std::atomic<int> known[2] = {{-1}, {-1}};       // device << 16 | clusters
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::atomic<int>& k = known[ctas == 4 ? 0 : 1];
+    if (k.load() >= 0 && k.load() >> 16 == dev) return k.load() & 0xffff;
+    static std::atomic<int> ready_dev{-1};
+    auto kern = int8_pair_kernel<false, true, true>;
+    if (!smem_ready(kern, Pair::SMEM, ready_dev)) return 0;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas * 64);
+    cfg.blockDim = dim3(Pair::THREADS);
+    cfg.dynamicSmemBytes = Pair::SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();   // not this call's error: no split then
+        return 0;
+    }
+    k.store(dev << 16 | n);
+    return n;
+}
+
+PairPlan pair_plan(const I8GemmArgs& g, int per, int tiles) {
     const long long pairs = g.num_sms / 2, nkb = (g.K + kKB - 1) / kKB;
     const long long w = static_cast<long long>(std::min(g.E, g.R)) * ((tiles + 1) / 2);
-    int best = 256;
+    PairPlan best{256, 1};
     long long best_cost = 0;
     for (int bt = 256; bt >= 64; bt /= 2) {
-        const long long waves = (w * ((per + bt - 1) / bt) + pairs - 1) / pairs;
-        const long long cost = waves * (nkb * std::max(2 * bt, (16384 + 64 * bt) / 58) + 3000);
-        if (best_cost == 0 || cost < best_cost) {
-            best = bt;
-            best_cost = cost;
+        const long long n = w * ((per + bt - 1) / bt);
+        const int kblock = std::max(2 * bt, (16384 + 64 * bt) / 58);
+        for (int S = 1; S <= 4; S *= 2) {
+            if (S > 1 && (g.E != 1 || nkb < 4 * S || n * S > pairs || n > pair_clusters(2 * S))) break;
+            const long long waves = S > 1 ? 1 : (n + pairs - 1) / pairs;
+            const long long cost =
+                waves * ((nkb + S - 1) / S * kblock + 3000) + (S > 1 ? 2000 + 16 * bt : 0);
+            if (best_cost == 0 || cost < best_cost) {
+                best = PairPlan{bt, S};
+                best_cost = cost;
+            }
         }
     }
     return best;
@@ -819,13 +907,21 @@ int launch_narrow(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& 
 }
 
 template <bool GATED, bool BF16>
-int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int num_sms,
+int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p, int S, int num_sms,
                 cudaStream_t stream) {
+    if (S > 1) {
+        static std::atomic<int> ready_dev{-1};
+        auto kern = int8_pair_kernel<GATED, BF16, true>;
+        if (!smem_ready(kern, Pair::SMEM, ready_dev)) return ST_CUDA;
+        const int tiles = (p.wtiles + 1) / 2 * ((p.R + p.bt - 1) / p.bt);
+        return launch_dependent(kern, dim3(tiles * 2 * S), dim3(Pair::THREADS), 2 * S, Pair::SMEM, stream, mw,
+                                mx, p, S) == cudaSuccess ? ST_OK : ST_CUDA;
+    }
     static std::atomic<int> ready_dev{-1};
-    auto kern = int8_pair_kernel<GATED, BF16>;
+    auto kern = int8_pair_kernel<GATED, BF16, false>;
     if (!smem_ready(kern, Pair::SMEM, ready_dev)) return ST_CUDA;
-    return launch_dependent(kern, dim3(num_sms & ~1), dim3(Pair::THREADS), 0, Pair::SMEM, stream, mw, mx,
-                            p) == cudaSuccess ? ST_OK : ST_CUDA;
+    return launch_dependent(kern, dim3(num_sms & ~1), dim3(Pair::THREADS), 2, Pair::SMEM, stream, mw, mx, p,
+                            1) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <bool GATED, bool BF16>
@@ -841,10 +937,11 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int tiles = weight_tiles(g);
     const int per = (g.R + g.E - 1) / g.E;   // rows per expert, balanced
     if (per > 128) {
-        p.bt = pair_tile(g, per, tiles);
+        const PairPlan plan = pair_plan(g, per, tiles);
+        p.bt = plan.bt;
         p.nst = Pair::stages(p.bt);
         if (!make_map(&mx, g.a, g.R, g.K, Pair::xbox(p.bt))) return ST_CUDA;
-        return launch_pair<GATED, BF16>(mw, mx, p, g.num_sms, stream);
+        return launch_pair<GATED, BF16>(mw, mx, p, plan.S, g.num_sms, stream);
     }
     // rows of one expert of a balanced routing, with three standard deviations
     const int want = g.E == 1 ? g.R : std::min(g.R, per + static_cast<int>(3.0f * sqrtf(per)));

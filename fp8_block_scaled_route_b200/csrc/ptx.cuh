@@ -436,13 +436,14 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a_desc, u
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives on the barrier at this offset in both CTAs of the pair when every
-// tcgen05 operation issued so far by this thread has completed.
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// Arrives on the barrier at this offset in the CTAs of `mask` (cluster ranks; the
+// pair's two) when every tcgen05 operation issued so far by this thread has
+// completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(mask)
         : "memory");
 }
 // The same on this CTA's barrier alone.

@@ -219,7 +219,8 @@ MOE_API int moe_router_score_route(const void* logits, int logits_dtype, const f
  *  q, q_scale    device, as above; unused with MOE_Q_NONE
  * 0 < eps <= 1.  H a multiple of 16 (128 with MOE_Q_FP8 and MOE_Q_MXFP8), at
  * most MOE_NORM_MAX_H (else MOE_ERR_UNSUPPORTED).  At least one of y and q is
- * written.  T = 0 is a no-op.  Buffers 16-byte aligned (q_scale 4). */
+ * written.  T = 0 is a no-op.  Buffers 16-byte aligned (q_scale 4); apart from
+ * the aliases named above no output overlaps another buffer. */
 #define MOE_Q_NONE 0
 #define MOE_Q_FP8 1
 #define MOE_Q_MXFP8 2
@@ -536,7 +537,8 @@ MOE_API int nvfp4_tile_scales(const uint8_t* sf_rowmajor, uint8_t* sf_tiled, int
  *            j < k, of q and q_scale; entries outside [0, R) are skipped (as
  *            moe_route_permute's -1).  NULL: row t to row t (k = 1, R >= T)
  *  q         device int8 [R, K] out;  q_scale device fp32 [R] out
- * Rows that no entry names are left as they were.  K a multiple of 16, at most
+ * Rows that no entry names are left as they were; entries in [0, R) are
+ * distinct (a row named twice ends up with a mixture).  K a multiple of 16, at most
  * MOE_NORM_MAX_H.  T = 0 is a no-op.  x, q 16-byte aligned. */
 MOE_API int int8_quantize(const void* x, int T, int K, int k, int R, const int32_t* inv_perm,
                           int8_t* q, float* q_scale, moe_stream_t stream);

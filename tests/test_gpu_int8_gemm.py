@@ -111,6 +111,15 @@ def test_skewed_and_empty(counts, gated):
     check(sum(counts) + 9, 320, 336, 4, gated, counts=counts, seed=2)
 
 
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("R,N,K", [(20, 256, 1024), (100, 512, 4096), (300, 512, 4096), (520, 640, 2048),
+                                   (2000, 256, 256)])
+def test_one_expert_with_fewer_rows(R, N, K, gated):
+    """One expert whose m_indptr names some of the R rows, or none of them."""
+    for n in (0, 1, R // 2, R - 1):
+        check(R, N, K, 1, gated, counts=[n], seed=n)
+
+
 @pytest.mark.parametrize("R", [3, 600])
 def test_largest_sums(R):
     """-128 * -128 over the longest K whose 32-bit sums cannot overflow."""

@@ -31,7 +31,8 @@ def _score(T=8, E=64, k=4, logits=FAKE, ids=FAKE, w=FAKE, logits_dtype="float32"
     (dict(group_top=3), INVALID), (dict(n_group=32, topk_group=1, k=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(logits=0), INVALID), (dict(ids=0), INVALID),
-    (dict(w=0), INVALID), (dict(T=1 << 28, k=32, E=64), UNSUPPORTED),
+    (dict(w=0), INVALID), (dict(T=1 << 28, k=32, E=64), UNSUPPORTED), (dict(logits=FAKE + 2), INVALID),
+    (dict(ids=FAKE + 1), INVALID), (dict(w=FAKE + 2), INVALID), (dict(bias=FAKE + 2), INVALID),
 ])
 def test_score_refusals(args, want):
     assert _score(**args) == want
@@ -43,6 +44,7 @@ def test_score_route_refusals():
                                           dims=(8, 64, 4), stream=0, check=False, **how)
     assert r(m=0) == INVALID
     assert r(perm=0) == INVALID
+    assert r(m=FAKE + 2) == INVALID and r(perm=FAKE + 1) == INVALID
     assert r(ws=0) == INVALID
     assert r(ws=FAKE + 4) == INVALID
     assert r(ws_bytes=64) == INVALID
@@ -76,7 +78,7 @@ def test_norm_refusals(args, want):
     (dict(T=-1), INVALID), (dict(K=0), INVALID), (dict(K=24), INVALID), (dict(K=32784), UNSUPPORTED),
     (dict(k=0), INVALID), (dict(k=2), INVALID), (dict(R=3), INVALID), (dict(x=0), INVALID),
     (dict(q=0), INVALID), (dict(s=0), INVALID), (dict(x=FAKE + 2), INVALID), (dict(q=FAKE + 8), INVALID),
-    (dict(R=-1), INVALID),
+    (dict(R=-1), INVALID), (dict(s=FAKE + 2), INVALID),
 ])
 def test_quantize_refusals(args, want):
     a = dict(T=4, K=64, k=1, R=4, x=FAKE, q=FAKE, s=FAKE) | args
@@ -90,7 +92,8 @@ def test_quantize_refusals(args, want):
     (dict(K=131072), UNSUPPORTED), (dict(N=33, gated=True), INVALID), (dict(od=2), INVALID),
     (dict(E=1024, N=1 << 21), UNSUPPORTED), (dict(a=0), INVALID), (dict(b=0), INVALID),
     (dict(sa=0), INVALID), (dict(sb=0), INVALID), (dict(out=0), INVALID), (dict(a=FAKE + 8), INVALID),
-    (dict(b=FAKE + 4), INVALID), (dict(out=FAKE + 2), INVALID),
+    (dict(b=FAKE + 4), INVALID), (dict(out=FAKE + 2), INVALID), (dict(sa=FAKE + 2), INVALID),
+    (dict(sb=FAKE + 1), INVALID), (dict(m=FAKE + 2), INVALID),
 ])
 def test_gemm_refusals(args, want):
     c = dict(R=8, N=32, K=64, E=1, m=FAKE, gated=False, od="bfloat16", a=FAKE, b=FAKE, sa=FAKE, sb=FAKE,
