@@ -530,7 +530,8 @@ def moe_get_device_status(ws=None, *, stream=None) -> int:
 
 # ---------------------------------------------------------------- scored router, norm, int8
 # These calls are a few microseconds of GPU work at decoding sizes, so their
-# marshalling is kept short: checks by identity, addresses as plain integers.
+# marshalling is kept short: tensors are checked by identity, and only a call
+# that fails the short check goes through the one that says what is wrong.
 _SCORING = {"softmax": 0, "sigmoid": 1}
 _Q_FORMAT = {"none": 0, "fp8": 1, "mxfp8": 2, "int8": 3}
 _MAJOR = {"K": 0, "MN": 1}
@@ -567,18 +568,22 @@ def _torch():
     return _tc
 
 
+def _is(t, dtype, shape, dev):
+    """A contiguous tensor of this dtype, shape and device."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev
+
+
 def _tensors(where, dev, *specs):
     """Checks tensors against (name, tensor, dtype or dtypes, shape or None):
-    raises ValueError for one that the C entry would misread.  None and raw
-    addresses pass."""
+    raises ValueError for one that the C entry would misread.  None passes."""
     for name, t, dtype, shape in specs:
-        if t is None or t.__class__ is int:
+        if t is None:
             continue
         ok = t.dtype in dtype if dtype.__class__ is tuple else t.dtype is dtype
         if not ok:
             raise ValueError(f"{where}: {name} is {t.dtype}, expected {dtype}")
         if shape is not None and t.shape != shape:
-            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {shape}")
+            raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if not t.is_contiguous():
             raise ValueError(f"{where}: {name} is not contiguous")
         if t.get_device() != dev:
@@ -605,22 +610,11 @@ def _call(where, fn, args, dev, stream, check):
     return st
 
 
-def _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group, group_top,
-                renorm, scale, dims, logits_dtype):
-    if dims is None:
-        tc = _torch()
-        T, E = logits.shape
-        k = topk_ids.shape[1]
-        dev = logits.get_device()
+def _score_check(where, tc, logits, topk_ids, topk_w, bias, T, E, k, dev):
+    if not (logits.dtype in tc.float and logits.is_contiguous() and _is(topk_ids, tc.i32, (T, k), dev)
+            and _is(topk_w, tc.f32, (T, k), dev) and (bias is None or _is(bias, tc.f32, (E,), dev))):
         _tensors(where, dev, ("logits", logits, tc.float, None), ("topk_ids", topk_ids, tc.i32, (T, k)),
                  ("topk_w", topk_w, tc.f32, (T, k)), ("bias", bias, tc.f32, (E,)))
-        dtype = tc.code[logits.dtype]
-    else:
-        T, E, k = dims
-        dev, dtype = None, _DTYPE.get(logits_dtype, logits_dtype)
-    return T, E, k, dev, (_addr(logits), dtype, _addr(bias), T, E, k, _SCORING.get(scoring, scoring),
-                          n_group, topk_group, group_top, 1 if renorm else 0, scale, _addr(topk_ids),
-                          _addr(topk_w))
 
 
 def moe_router_score_topk(logits, topk_ids, topk_w, *, bias=None, scoring="softmax", n_group=1,
@@ -630,9 +624,19 @@ def moe_router_score_topk(logits, topk_ids, topk_w, *, bias=None, scoring="softm
     [T, k], topk_w fp32 [T, k].  scoring "softmax" or "sigmoid".
     dims = (T, E, k) and logits_dtype when raw addresses are passed."""
     where = "moe_router_score_topk"
-    _, _, _, dev, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
-                                  group_top, renorm, scale, dims, logits_dtype)
-    return _call(where, lib().moe_router_score_topk, a, dev, stream, check)
+    if dims is None:
+        tc = _tc or _torch()
+        T, E = logits.shape
+        k = topk_ids.shape[1]
+        dev = logits.get_device()
+        _score_check(where, tc, logits, topk_ids, topk_w, bias, T, E, k, dev)
+        dtype = tc.code[logits.dtype]
+    else:
+        T, E, k = dims
+        dev, dtype = None, _DTYPE.get(logits_dtype, logits_dtype)
+    a = (_addr(logits), dtype, _addr(bias), T, E, k, _SCORING.get(scoring, scoring), n_group, topk_group,
+         group_top, 1 if renorm else 0, scale, _addr(topk_ids), _addr(topk_w))
+    return _call(where, (_lib or lib()).moe_router_score_topk, a, dev, stream, check)
 
 
 def moe_router_score_route(logits, topk_ids, topk_w, m_indptr, perm, inv_perm, ws, ws_bytes=None, *,
@@ -642,16 +646,27 @@ def moe_router_score_route(logits, topk_ids, topk_w, m_indptr, perm, inv_perm, w
     """moe_router_score_topk + moe_route_permute in one call.
     dims = (T, E, k) and logits_dtype when raw addresses are passed."""
     where = "moe_router_score_route"
-    T, E, k, dev, a = _score_args(where, logits, topk_ids, topk_w, bias, scoring, n_group, topk_group,
-                                  group_top, renorm, scale, dims, logits_dtype)
     if dims is None:
-        tc = _torch()
-        _tensors(where, dev, ("m_indptr", m_indptr, tc.i32, (E + 1,)), ("perm", perm, tc.i32, (T * k,)),
-                 ("inv_perm", inv_perm, tc.i32, (T * k,)), ("ws", ws, tc.u8, None))
+        tc = _tc or _torch()
+        T, E = logits.shape
+        k = topk_ids.shape[1]
+        dev = logits.get_device()
+        _score_check(where, tc, logits, topk_ids, topk_w, bias, T, E, k, dev)
+        if not (_is(m_indptr, tc.i32, (E + 1,), dev) and _is(perm, tc.i32, (T * k,), dev)
+                and (inv_perm is None or _is(inv_perm, tc.i32, (T * k,), dev))
+                and ws.dtype is tc.u8 and ws.is_contiguous() and ws.get_device() == dev):
+            _tensors(where, dev, ("m_indptr", m_indptr, tc.i32, (E + 1,)), ("perm", perm, tc.i32, (T * k,)),
+                     ("inv_perm", inv_perm, tc.i32, (T * k,)), ("ws", ws, tc.u8, None))
+        dtype = tc.code[logits.dtype]
+    else:
+        T, E, k = dims
+        dev, dtype = None, _DTYPE.get(logits_dtype, logits_dtype)
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size()
-    a += (_addr(m_indptr), _addr(perm), _addr(inv_perm), _addr(ws), ws_bytes)
-    return _call(where, lib().moe_router_score_route, a, dev, stream, check)
+    a = (_addr(logits), dtype, _addr(bias), T, E, k, _SCORING.get(scoring, scoring), n_group, topk_group,
+         group_top, 1 if renorm else 0, scale, _addr(topk_ids), _addr(topk_w), _addr(m_indptr), _addr(perm),
+         _addr(inv_perm), _addr(ws), ws_bytes)
+    return _call(where, (_lib or lib()).moe_router_score_route, a, dev, stream, check)
 
 
 def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=None, q_format="none",
@@ -665,13 +680,19 @@ def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=Non
     where = "moe_rmsnorm_quant"
     fmt, mn = _Q_FORMAT.get(q_format, q_format), _MAJOR.get(scale_major, scale_major)
     if dims is None:
-        tc = _torch()
+        tc = _tc or _torch()
         shape = x.shape
         T, H = shape
         dev = x.get_device()
-        _tensors(where, dev, ("x", x, tc.bf16, None), ("residual", residual, tc.bf16, shape),
-                 ("weight", weight, tc.float, (H,)), ("residual_out", residual_out, tc.bf16, shape),
-                 ("y", y, tc.bf16, shape))
+        bf16 = tc.bf16
+        if not (x.dtype is bf16 and x.is_contiguous()
+                and (residual is None or _is(residual, bf16, shape, dev))
+                and weight.dtype in tc.float and _is(weight, weight.dtype, (H,), dev)
+                and (residual_out is None or _is(residual_out, bf16, shape, dev))
+                and (y is None or _is(y, bf16, shape, dev))):
+            _tensors(where, dev, ("x", x, bf16, None), ("residual", residual, bf16, shape),
+                     ("weight", weight, tc.float, (H,)), ("residual_out", residual_out, bf16, shape),
+                     ("y", y, bf16, shape))
         if fmt == 1:
             _tensors(where, dev, ("q", q, tc.e4m3, shape),
                      ("q_scale", q_scale, tc.f32, (H // 128, T) if mn == 1 else (T, H // 128)))
@@ -686,7 +707,7 @@ def moe_rmsnorm_quant(x, weight, eps, *, residual=None, residual_out=None, y=Non
         dev, wd = None, _DTYPE.get(weight_dtype, weight_dtype)
     a = (_addr(x), _addr(residual), _addr(weight), wd, eps, T, H, _addr(residual_out), _addr(y), fmt,
          _addr(q), _addr(q_scale), mn)
-    return _call(where, lib().moe_rmsnorm_quant, a, dev, stream, check)
+    return _call(where, (_lib or lib()).moe_rmsnorm_quant, a, dev, stream, check)
 
 
 def int8_quantize(x, q, q_scale, *, inv_perm=None, k=1, dims=None, stream=None, check=True) -> int:
@@ -695,19 +716,20 @@ def int8_quantize(x, q, q_scale, *, inv_perm=None, k=1, dims=None, stream=None, 
     raw addresses are passed."""
     where = "int8_quantize"
     if dims is None:
-        tc = _torch()
+        tc = _tc or _torch()
         T, K = x.shape
         R = q.shape[0]
         dev = x.get_device()
-        _tensors(where, dev, ("x", x, tc.bf16, None), ("q", q, tc.i8, (R, K)),
-                 ("q_scale", q_scale, tc.f32, (R,)), ("inv_perm", inv_perm, tc.i32, None))
-        if inv_perm is not None and inv_perm.numel() != T * k:
-            raise ValueError(f"{where}: inv_perm has {inv_perm.numel()} entries, expected {T * k}")
+        if not (x.dtype is tc.bf16 and x.is_contiguous() and _is(q, tc.i8, (R, K), dev)
+                and _is(q_scale, tc.f32, (R,), dev)
+                and (inv_perm is None or _is(inv_perm, tc.i32, (T * k,), dev))):
+            _tensors(where, dev, ("x", x, tc.bf16, None), ("q", q, tc.i8, (R, K)),
+                     ("q_scale", q_scale, tc.f32, (R,)), ("inv_perm", inv_perm, tc.i32, (T * k,)))
     else:
         T, K, R = dims
         dev = None
     a = (_addr(x), T, K, k, R, _addr(inv_perm), _addr(q), _addr(q_scale))
-    return _call(where, lib().int8_quantize, a, dev, stream, check)
+    return _call(where, (_lib or lib()).int8_quantize, a, dev, stream, check)
 
 
 def int8_moe_gemm(a, b, a_scale, b_scale, out, *, m_indptr=None, is_gated=False, dims=None,
@@ -718,23 +740,28 @@ def int8_moe_gemm(a, b, a_scale, b_scale, out, *, m_indptr=None, is_gated=False,
     dims = (R, N, K, E) and out_dtype when raw addresses are passed."""
     where = "int8_moe_gemm"
     if dims is None:
-        tc = _torch()
+        tc = _tc or _torch()
         R, K = a.shape
         bs = b.shape
         E, N = (bs[0], bs[1]) if len(bs) == 3 else (1, bs[0])
         dev = a.get_device()
-        _tensors(where, dev, ("a", a, tc.i8, None), ("b", b, tc.i8, (E, N, K) if len(bs) == 3 else (N, K)),
-                 ("a_scale", a_scale, tc.f32, (R,)),
-                 ("b_scale", b_scale, tc.f32, (N,) if b_scale.dim() == 1 and E == 1 else (E, N)),
-                 ("m_indptr", m_indptr, tc.i32, (E + 1,)),
-                 ("out", out, tc.float, (R, N // 2 if is_gated else N)))
+        n_out = N // 2 if is_gated else N
+        s_shape = (N,) if E == 1 and b_scale.dim() == 1 else (E, N)
+        if not (a.dtype is tc.i8 and a.is_contiguous() and bs[-1] == K and _is(b, tc.i8, bs, dev)
+                and _is(a_scale, tc.f32, (R,), dev) and _is(b_scale, tc.f32, s_shape, dev)
+                and (m_indptr is None or _is(m_indptr, tc.i32, (E + 1,), dev))
+                and out.dtype in tc.float and _is(out, out.dtype, (R, n_out), dev)):
+            _tensors(where, dev, ("a", a, tc.i8, None),
+                     ("b", b, tc.i8, (E, N, K) if len(bs) == 3 else (N, K)),
+                     ("a_scale", a_scale, tc.f32, (R,)), ("b_scale", b_scale, tc.f32, s_shape),
+                     ("m_indptr", m_indptr, tc.i32, (E + 1,)), ("out", out, tc.float, (R, n_out)))
         od = tc.code[out.dtype]
     else:
         R, N, K, E = dims
         dev, od = None, _DTYPE.get(out_dtype, out_dtype)
     args = (_addr(a), _addr(b), _addr(a_scale), _addr(b_scale), _addr(m_indptr), _addr(out), od, R, N, K,
             E, 1 if is_gated else 0)
-    return _call(where, lib().int8_moe_gemm, args, dev, stream, check)
+    return _call(where, (_lib or lib()).int8_moe_gemm, args, dev, stream, check)
 
 
 # ---------------------------------------------------------------- expert parallelism
