@@ -13,9 +13,9 @@
 // One warp per token, lane l holding experts l + 32 i.  Bound: integer and
 // compare instructions (8192 x 256 logits are 8 MB, 1.3 us of HBM), so the
 // selection avoids a warp-wide argmax per winner: the k-th largest of the 32
-// lane maxima bounds the k-th largest value from below, about k + 1 (k = 8) to
-// 1.4 k (k = 16) values reach that bound, and those, one per lane, find their
-// rank by comparing with one another.
+// lane maxima bounds the k-th largest value from below, few more than k values
+// reach that bound (9 for k = 8), and those, one per lane, find their rank by
+// comparing with one another.
 //
 // The choice is that of 64-bit values at 32-bit speed: c is computed in fp32
 // with a bounded error (score_tol).  Where two of the candidates lie closer
@@ -272,7 +272,11 @@ __host__ __device__ constexpr int scratch_floats(int E, bool groups) {
     return groups && 2 * E > 4 * 32 * CPL ? (2 * E + 3) & ~3 : 4 * 32 * CPL;   // 16-byte aligned
 }
 
-// One token by one warp.  k <= 16 CPL.  hist: the CTA's expert counts, or null.
+// One token by one warp.  CPL: places for candidates a lane, and lane maxima
+// that bound them.  The candidates are as many as it takes to meet k of the 32
+// CPL maxima: 15 of 32 places for k = 12, 22 for 16 (one token in 200 has more
+// than 32 and is decided in 64 bits: 4096 x 1024 top-16 took 49 us, with two
+// places a lane 18), 44 of 64 for k = 32.  hist: the CTA's expert counts, or null.
 template <int PER, int CPL, typename LT>
 __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* scratch, int* hist) {
     const int lane = threadIdx.x & 31;
@@ -504,7 +508,7 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
 constexpr int kScoreWarps = 4;
 
 template <int PER, int CPL, typename LT>
-__global__ void __launch_bounds__(32 * kScoreWarps, PER <= 8 ? 7 : 4) score_kernel(const ScoreArgs a) {
+__global__ void __launch_bounds__(32 * kScoreWarps, PER <= 16 ? 7 : 6) score_kernel(const ScoreArgs a) {
     extern __shared__ __align__(16) float scratch[];
     const int warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kScoreWarps + warp;
@@ -828,7 +832,7 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
 
 template <int PER, typename LT>
 int launch_k(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
-    return a.k <= 16 ? launch_inst<PER, 1, LT>(a, r, s) : launch_inst<PER, 2, LT>(a, r, s);
+    return a.k <= 12 ? launch_inst<PER, 1, LT>(a, r, s) : launch_inst<PER, 2, LT>(a, r, s);
 }
 
 template <typename LT>
