@@ -249,12 +249,16 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 2 ? 512 : 1024, V == 2 && !W
 
 // Row t of x [T, K] -> int8 codes and scale at rows inv_perm[t*k + j] (row t
 // when inv_perm is null); entries outside [0, R) are skipped.
-template <bool WARP, int V>
-__global__ void __launch_bounds__(WARP ? 256 : 1024)
+// WIDE: CTAs of more than 256 threads, or several copies a row.
+template <bool WARP, int V, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
     int8_quant_kernel(const __nv_bfloat16* __restrict__ xin, int T, int K, int k, int R,
                       const int32_t* __restrict__ inv_perm, int8_t* __restrict__ q,
                       float* __restrict__ q_scale) {
-    // four groups a thread: 65536 x 2048 92 us with one, 68 with four
+    // 65536 x 2048: one group a thread 92 us, four 68, and 59.5 (1.04 of the copy
+    // rate) with six CTAs of 256 threads an SM (40 registers); with eight copies a
+    // row the stores bound it, and fewer CTAs keep their runs longer: 8192 x 7168
+    // 95 us against 101
     __shared__ float red[32];
     pdl_launch();
     pdl_wait();
@@ -306,9 +310,17 @@ dim3 row_block(int nvec, int V) {
     return dim3(tpr, tpr <= 128 ? 256 / tpr : 1);
 }
 
-// One group a thread (a row spread over as many warps as it can) where there is
-// at most a row for each SM: 64 x 7168 3.5 us against 4.4 with four.
-bool one_group(int T, int nvec, int num_sms) { return T <= num_sms && nvec > 32 && nvec <= 1024; }
+// Groups a thread.  Few rows: one, a row spread over as many warps as it can,
+// while all of them are resident at about half the SMs' threads (64 x 7168 norm
+// 3.5 us against 4.4 with four; 600 x 2048 4.1 against 4.6 with two).  Then two,
+// and for the quantiser, which keeps less of a row, four above twice as much work
+// (2400 x 4096 8.5 us with two, 7.0 with four).
+int groups_a_thread(int T, int nvec, int num_sms, int most) {
+    const long long work = static_cast<long long>(T) * nvec, half = 1100ll * num_sms;
+    if (nvec <= 32 || (nvec <= 1024 && work <= half)) return 1;
+    if (nvec <= 1024 && (most == 2 || work <= 2 * half)) return 2;
+    return 4;
+}
 
 template <bool WARP, int V>
 int launch_norm(const RmsNormArgs& p, dim3 block, cudaStream_t s) {
@@ -324,9 +336,10 @@ template <bool WARP, int V>
 int launch_q8(const void* x, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
               float* q_scale, dim3 block, cudaStream_t s) {
     const unsigned grid = (static_cast<unsigned>(T) + block.y - 1) / block.y;
-    return launch_dependent(int8_quant_kernel<WARP, V>, dim3(grid), block, 0, 0, s,
-                            static_cast<const __nv_bfloat16*>(x), T, K, k, R, inv_perm, q, q_scale) ==
-                   cudaSuccess ? ST_OK : ST_CUDA;
+    const bool wide = !WARP && (k > 1 || block.x * block.y > 256);
+    auto kern = wide ? int8_quant_kernel<WARP, V, !WARP> : int8_quant_kernel<WARP, V, false>;
+    return launch_dependent(kern, dim3(grid), block, 0, 0, s, static_cast<const __nv_bfloat16*>(x), T, K, k,
+                            R, inv_perm, q, q_scale) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 }  // namespace
@@ -334,7 +347,7 @@ int launch_q8(const void* x, int T, int K, int k, int R, const int32_t* inv_perm
 int launch_rmsnorm(const RmsNormArgs& p, int num_sms, cudaStream_t s) {
     if (p.T == 0) return ST_OK;
     const int nvec = p.H >> 3;
-    const int per_thread = one_group(p.T, nvec, num_sms) || nvec <= 32 ? 1 : nvec <= 1024 ? 2 : 4;
+    const int per_thread = groups_a_thread(p.T, nvec, num_sms, 2);
     const dim3 block = row_block(nvec, per_thread);
     if (per_thread == 1)
         return block.x == 32 ? launch_norm<true, 1>(p, block, s) : launch_norm<false, 1>(p, block, s);
@@ -347,12 +360,17 @@ int launch_int8_quant(const void* x, int T, int K, int k, int R, const int32_t* 
                       int8_t* q, float* q_scale, int num_sms, cudaStream_t s) {
     if (T == 0) return ST_OK;
     const int nvec = K >> 3;
-    if (one_group(T, nvec, num_sms))
-        return launch_q8<false, 1>(x, T, K, k, R, inv_perm, q, q_scale, row_block(nvec, 1), s);
-    if (nvec <= 32) return launch_q8<true, 1>(x, T, K, k, R, inv_perm, q, q_scale, row_block(nvec, 1), s);
-    const dim3 block = row_block(nvec, 4);
-    return block.x == 32 ? launch_q8<true, 4>(x, T, K, k, R, inv_perm, q, q_scale, block, s)
-                         : launch_q8<false, 4>(x, T, K, k, R, inv_perm, q, q_scale, block, s);
+    const int per_thread = groups_a_thread(T, nvec, num_sms, 4);
+    const dim3 block = row_block(nvec, per_thread);
+    const bool warp = block.x == 32;
+    if (per_thread == 1)
+        return warp ? launch_q8<true, 1>(x, T, K, k, R, inv_perm, q, q_scale, block, s)
+                    : launch_q8<false, 1>(x, T, K, k, R, inv_perm, q, q_scale, block, s);
+    if (per_thread == 2)
+        return warp ? launch_q8<true, 2>(x, T, K, k, R, inv_perm, q, q_scale, block, s)
+                    : launch_q8<false, 2>(x, T, K, k, R, inv_perm, q, q_scale, block, s);
+    return warp ? launch_q8<true, 4>(x, T, K, k, R, inv_perm, q, q_scale, block, s)
+                : launch_q8<false, 4>(x, T, K, k, R, inv_perm, q, q_scale, block, s);
 }
 
 }  // namespace moe
