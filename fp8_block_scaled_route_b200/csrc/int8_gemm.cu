@@ -44,7 +44,7 @@ struct I8Params {
     const float* b_scale;
     const int32_t* m_indptr;
     void* out;
-    int R, N, K, E, nkb;
+    int R, N, E, nkb;
     int wtiles;   // narrow kernel: weight tiles of an expert
     int bt;       // pair kernel: token rows of a tile (64, 128 or 256)
     int nst;      // pair kernel: stages
@@ -263,7 +263,7 @@ __device__ __forceinline__ Item item_of(const I8Params& p, int bt, const int* st
 // ring of NST stages.
 //  SPLIT = false: CTAs walk over the item table, the next items' loads running
 //    under an item's epilogue (4096 rows of 128 experts 1536 x 2048 gated: one
-//    CTA per tile 73 us, walking 69.5; and a crowded expert's token blocks are
+//    CTA per tile 73 us, walking 70.8; and a crowded expert's token blocks are
 //    items of their own, where a CTA that looped over them took up to twice as
 //    long as the rest).
 //  SPLIT = true: few tiles and at most BT rows in all; a cluster of S CTAs
@@ -546,7 +546,6 @@ struct Pair {
     static constexpr int xbox(int bt) { return bt / 2; }   // token rows per TMA box
 };
 
-//
 // SPLIT: few tiles (one expert); a cluster of S pairs shares each, a pair summing
 // the S-th part of the K range.  Every CTA then lays its 128 weight rows' sums out
 // in shared memory and adds up, over the pairs, every S-th 16 columns of them.
@@ -792,8 +791,8 @@ bool make_map(CUtensorMap* m, const void* ptr, long long rows, int cols, int box
     return encode(m, ptr, 2, dims, strides, box);
 }
 
-// Map of gated weights [E, 2, N/2, K] whose boxes are two granules: 16 gate
-// rows, their 16 up rows, twice.
+// Map of gated weights [E, 2, N/2, K] whose boxes are four granules: 16 gate
+// rows, their 16 up rows, four times.
 bool make_gated_map(CUtensorMap* m, const void* ptr, int E, int N, int K) {
     const cuuint64_t k = K, half = N / 2;
     const cuuint64_t dims[5] = {k, kGran, 2, half / kGran, static_cast<cuuint64_t>(E)};
@@ -924,11 +923,17 @@ int launch_pair(const CUtensorMap& mw, const CUtensorMap& mx, const I8Params& p,
                             1) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
+// Whether the item table's sums stay below 2^31 whatever m_indptr holds (each
+// expert's rows are clamped to [0, R], but a wrong table may name rows twice).
+bool items_fit(const I8GemmArgs& g, int bt, int tiles) {
+    return static_cast<long long>(g.E) * ((g.R + static_cast<long long>(bt) - 1) / bt) * tiles < 0x7fffffffll;
+}
+
 template <bool GATED, bool BF16>
 int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     const int nkb = (g.K + kKB - 1) / kKB;
     const int w_gran = GATED && (g.N / 2) % kGran ? 1 : 0;
-    I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.K, g.E, nkb, weight_tiles(g), 0, 0, w_gran,
+    I8Params p{g.a_scale, g.b_scale, g.m_indptr, g.out, g.R, g.N, g.E, nkb, weight_tiles(g), 0, 0, w_gran,
                      g.status, g.timeout_ns};
     CUtensorMap mw, mx;
     if (GATED && !w_gran ? !make_gated_map(&mw, g.b, g.E, g.N, g.K)
@@ -939,6 +944,7 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
     if (per > 128) {
         const PairPlan plan = pair_plan(g, per, tiles);
         p.bt = plan.bt;
+        if (!items_fit(g, p.bt, tiles)) return ST_UNSUPPORTED;
         p.nst = Pair::stages(p.bt);
         if (!make_map(&mx, g.a, g.R, g.K, Pair::xbox(p.bt))) return ST_CUDA;
         return launch_pair<GATED, BF16>(mw, mx, p, plan.S, g.num_sms, stream);
@@ -952,6 +958,7 @@ int launch_t(const I8GemmArgs& g, cudaStream_t stream) {
         const long long units = static_cast<long long>(tiles) * std::min(g.E, g.R);
         while (S < kMaxSplit && units * S * 2 <= 2 * g.num_sms && nkb >= S * 2 * 4) S *= 2;
     }
+    if (!items_fit(g, bt, tiles)) return ST_UNSUPPORTED;
     if (!make_map(&mx, g.a, g.R, g.K, bt < 64 ? bt : 64)) return ST_CUDA;
     switch (bt) {
         case 16: return launch_narrow<16, GATED, BF16>(mw, mx, p, S, g.num_sms, stream);

@@ -27,7 +27,9 @@ inline cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block
         at[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) cudaGetLastError();   // reported by this call, not by the next one
+    return e;
 }
 
 // Epilogue of the grouped GEMM.

@@ -667,7 +667,9 @@ MOE_API int moe_combine(const float* y, const int32_t* row_of_pair, const float*
 /* Synchronises `stream`, then returns the device status word written by the
  * last calls that used `ws` (a moe_fp8_fused / moe_route_permute workspace),
  * or, with ws = NULL, the library's own word used by fp8_groupwise_moe_gemm
- * and swiglu_mxfp8_quant.  Each entry point clears its word when it starts.
+ * and swiglu_mxfp8_quant, and if that is clear, the word of int8_moe_gemm.
+ * Each entry point clears its word when it starts, except int8_moe_gemm, whose
+ * word stays until this call has read it.
  * Returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_BAD_EXPERT_ID or
  * MOE_ERR_CUDA (the synchronise or the read failed). */
 MOE_API int moe_get_device_status(const void* ws, moe_stream_t stream);

@@ -180,6 +180,25 @@ def test_far_logits(scoring):
     check(logits.cuda(), 2, torch.tensor([0.5, 0.4, 0.3, -1.0]).cuda(), scoring, span=210.0)
 
 
+@pytest.mark.parametrize("T,E,k", [(5000, 40, 1), (9000, 16, 1), (20000, 64, 8), (2049, 512, 32), (16384, 1024, 8)])
+def test_many_tokens(T, E, k):
+    """Each way of grouping (one launch after the router, three, two with counts)."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    ids, w, m, perm, inv, ws = buffers(T, E, k)
+    moe.moe_router_score_route(logits, ids, w, m, perm, inv, ws)
+    assert moe.moe_get_device_status(ws) == moe.MOE_OK
+    order = torch.sort(logits, dim=1, descending=True, stable=True)
+    assert torch.equal(ids.long(), order.indices[:, :k])
+    want = torch.softmax(order.values[:, :k].double(), 1)
+    # an exponential's argument rounding (9 ulps), itself, a sum of 32, two products
+    assert bool(((w.double() - want).abs() <= 48 * 2.0 ** -24 * want).all())
+    flat = ids.flatten().long()
+    assert torch.equal(perm.long(), torch.sort(flat, stable=True).indices)
+    assert torch.equal(inv.long()[perm.long()], torch.arange(T * k, device="cuda"))
+    assert torch.equal(m[1:].long(), torch.bincount(flat, minlength=E).cumsum(0)) and int(m[0]) == 0
+
+
 def test_no_tokens():
     ids, w, m, perm, inv, ws = buffers(0, 16, 4)
     logits = torch.empty(0, 16, device="cuda")
