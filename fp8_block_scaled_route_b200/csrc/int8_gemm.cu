@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "ptx_cluster.cuh"
 
 namespace moe {
 

@@ -5,7 +5,7 @@
 
 namespace moe {
 
-// Launch of a kernel that calls pdl_wait (ptx.cuh): dependent launch, and a
+// Launch of a kernel that calls pdl_wait (ptx_cluster.cuh): dependent launch, and a
 // cluster of `cluster` CTAs along x when above 0.
 template <typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, dim3 block, unsigned cluster,

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ptx_cluster.cuh"
 
 namespace moe {
 
