@@ -606,7 +606,7 @@ __host__ __device__ inline int bits_of(int E) {
 // one CTA alone would issue 64 tokens' selection in ~6 us.
 constexpr int kSmallWarps = 16;
 constexpr int kSmallCluster = 8;
-constexpr int kSmallTokens = 256;
+constexpr int kSmallTokens = 128;
 constexpr int kSmallSteps = 9;
 constexpr int kSmallPairs = kSmallWarps * kSmallSteps * 32;
 
@@ -703,10 +703,12 @@ __global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
 // have one or two steps of 32 pairs each.
 constexpr int kPlaceWarps = 32;
 
+// Without counts from the first launch (COUNT: few chunks, after the router
+// alone), every CTA counts all R ids itself, 8 a thread; the first clears status.
+template <bool COUNT>
 __global__ void __launch_bounds__(32 * kPlaceWarps)
-    place_kernel(const int32_t* __restrict__ ids, int R, int E, int nbits, int chunk_pairs,
-                 const int32_t* __restrict__ chunk_hist, int32_t* m_indptr, int32_t* perm,
-                 int32_t* inv_perm) {
+    place_kernel(const int32_t* ids, int R, int E, int nbits, int chunk_pairs, const int32_t* chunk_hist,
+                 int32_t* m_indptr, int32_t* perm, int32_t* inv_perm, int* status) {
     extern __shared__ __align__(16) int smem[];
     __shared__ int warp_tot[kPlaceWarps];
     __shared__ int part_total[32 * kPlaceWarps], part_before[32 * kPlaceWarps];
@@ -714,9 +716,31 @@ __global__ void __launch_bounds__(32 * kPlaceWarps)
     int* base = cnt + kPlaceWarps * E;     // [E]
     const int nchunks = gridDim.x, chunk = blockIdx.x;
     const int e = threadIdx.x & ((1 << nbits) - 1), g = threadIdx.x >> nbits;   // E <= 2^nbits <= 1024
-    const int G = (32 * kPlaceWarps) >> nbits;
+    const int G = COUNT ? 1 : (32 * kPlaceWarps) >> nbits;
+    const int first = chunk * chunk_pairs;
+    if constexpr (COUNT) {
+        part_total[threadIdx.x] = part_before[threadIdx.x] = 0;
+        __syncthreads();
+    }
     pdl_wait();
     int total = 0, before = 0;
+    if constexpr (COUNT) {
+        if (chunk == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
+        for (int p0 = threadIdx.x; p0 < R; p0 += 8 * 32 * kPlaceWarps) {
+            int id[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int p = p0 + i * 32 * kPlaceWarps;
+                id[i] = p < R ? __ldcg(ids + p) : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (id[i] >= 0) {
+                    atomicAdd(&part_total[id[i]], 1);
+                    if (p0 + i * 32 * kPlaceWarps < first) atomicAdd(&part_before[id[i]], 1);
+                }
+        }
+    } else {
     for (int c0 = g; c0 < nchunks; c0 += 16 * G) {
         int h[16];
 #pragma unroll
@@ -732,9 +756,9 @@ __global__ void __launch_bounds__(32 * kPlaceWarps)
     }
     part_total[threadIdx.x] = total;
     part_before[threadIdx.x] = before;
+    }
     for (int i = threadIdx.x; i < kPlaceWarps * E; i += 32 * kPlaceWarps) cnt[i] = 0;
     __syncthreads();
-    const int first = chunk * chunk_pairs;
     Segment<kPlaceWarps, 2> seg;
     count_pairs(seg, ids, first, min(chunk_pairs, R - first), E, nbits, cnt);
     const bool mine = threadIdx.x < E;     // one thread an expert from here
@@ -776,14 +800,15 @@ bool smem_ready(Kern kern, size_t bytes, std::atomic<int>& ready_dev) {
     return true;
 }
 
+template <bool COUNT>
 int launch_place(const RouteArgs& r, int chunk_pairs, int nchunks, cudaStream_t s) {
     static std::atomic<int> ready{-1};
     const size_t smem = (kPlaceWarps + 1ull) * r.E * sizeof(int);
-    if (!smem_ready(place_kernel, smem, ready)) return ST_CUDA;
-    return launch_dependent(place_kernel, dim3(nchunks), dim3(32 * kPlaceWarps), 0, smem, s, r.topk_ids,
+    if (!smem_ready(place_kernel<COUNT>, smem, ready)) return ST_CUDA;
+    return launch_dependent(place_kernel<COUNT>, dim3(nchunks), dim3(32 * kPlaceWarps), 0, smem, s, r.topk_ids,
                             r.T * r.k, r.E, bits_of(r.E), chunk_pairs,
-                            static_cast<const int32_t*>(r.chunk_hist), r.m_indptr, r.perm, r.inv_perm) ==
-                   cudaSuccess ? ST_OK : ST_CUDA;
+                            static_cast<const int32_t*>(r.chunk_hist), r.m_indptr, r.perm, r.inv_perm,
+                            r.status) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <int PER, int CPL, typename LT>
@@ -803,7 +828,8 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
     // counts fit the workspace's
     const int chunk_tokens = (kRouteChunk + a.k - 1) / a.k;
     const int nchunks = (a.T + chunk_tokens - 1) / chunk_tokens;
-    if (r && nchunks <= kMaxChunks && a.k >= 2) {
+    const bool count_all = route_single_launch(R);   // at most 8 chunks of pairs
+    if (r && !count_all && nchunks <= kMaxChunks && a.k >= 2) {
         static std::atomic<int> ready{-1};
         const size_t smem = kChunkWarps * sf + static_cast<size_t>(a.E) * sizeof(int);
         const int C = 8;
@@ -812,7 +838,7 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
         if (launch_dependent(kern, dim3(nchunks * C), dim3(32 * kChunkWarps), C, smem, s, a, r->chunk_hist,
                              r->status, chunk_tokens, C) != cudaSuccess)
             return ST_CUDA;
-        return launch_place(*r, chunk_tokens * a.k, nchunks, s);
+        return launch_place<false>(*r, chunk_tokens * a.k, nchunks, s);
     }
     if (a.T > 0) {
         static std::atomic<int> ready{-1};
@@ -823,10 +849,10 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
             return ST_CUDA;
     }
     if (!r) return ST_OK;
+    if (count_all && R > 0) return launch_place<true>(*r, kRouteChunk, (R + kRouteChunk - 1) / kRouteChunk, s);
     RouteArgs rr = *r;
     rr.clear_status = 1;
-    if (!route_single_launch(R) &&
-        cudaMemsetAsync(r->status, 0, sizeof(int) * kStatusInts, s) != cudaSuccess)
+    if (R > 0 && cudaMemsetAsync(r->status, 0, sizeof(int) * kStatusInts, s) != cudaSuccess)
         return ST_CUDA;
     return launch_route_permute(rr, s);
 }
