@@ -277,9 +277,9 @@ __host__ __device__ constexpr int scratch_floats(int E, bool groups) {
 // that bound them.  The candidates are as many as it takes to meet k of the 32
 // CPL maxima: 15 of 32 places for k = 12, 22 for 16 (one token in 200 has more
 // than 32 and is decided in 64 bits: 4096 x 1024 top-16 took 49 us, with two
-// places a lane 18), 44 of 64 for k = 32.  hist: the CTA's expert counts, or null.
+// places a lane 18), 44 of 64 for k = 32.
 template <int PER, int CPL, typename LT>
-__device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* scratch, int* hist) {
+__device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* scratch) {
     const int lane = threadIdx.x & 31;
     const LT* l = static_cast<const LT*>(a.logits) + static_cast<long long>(t) * a.E;
     const bool sums = a.n_group > 1 && a.group_top == 2;   // group values add scores up
@@ -502,7 +502,6 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
             const long long at = static_cast<long long>(t) * a.k + rank[q];
             a.ids[at] = expert[q];
             a.w[at] = u[q] * a.scale;
-            if (hist) atomicAdd(&hist[expert[q]], 1);
         }
 }
 
@@ -516,7 +515,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, PER <= 16 ? 7 : 6) score_ker
     pdl_launch();
     pdl_wait();
     if (t >= a.T) return;
-    score_token<PER, CPL, LT>(a, t, scratch + warp * scratch_floats<CPL>(a.E, a.n_group > 1), nullptr);
+    score_token<PER, CPL, LT>(a, t, scratch + warp * scratch_floats<CPL>(a.E, a.n_group > 1));
 }
 
 // ------------------------------------------------------------ grouping
@@ -607,8 +606,7 @@ __host__ __device__ inline int bits_of(int E) {
 constexpr int kSmallWarps = 16;
 constexpr int kSmallCluster = 8;
 constexpr int kSmallTokens = 128;
-constexpr int kSmallSteps = 9;
-constexpr int kSmallPairs = kSmallWarps * kSmallSteps * 32;
+constexpr int kSmallSteps = kSmallTokens * 32 / (kSmallWarps * 32);   // steps of 32 pairs a warp, k <= 32
 
 template <int PER, int CPL, typename LT>
 __global__ void __launch_bounds__(32 * kSmallWarps)
@@ -628,7 +626,7 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
         if (threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
     }
     for (int t = rank + kSmallCluster * warp; t < a.T; t += kSmallCluster * kSmallWarps)
-        score_token<PER, CPL, LT>(a, t, scratch + warp * sf, nullptr);
+        score_token<PER, CPL, LT>(a, t, scratch + warp * sf);
     __syncwarp();
     cluster_sync_all();      // every CTA's ids are visible
     if (rank != 0) return;
@@ -664,51 +662,80 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
     place_pairs(seg, a.E, cnt, base, perm, inv_perm);
 }
 
-// More tokens, first launch: a cluster of CTAs routes one chunk of tokens
-// (about 1024 pairs) and writes the chunk's expert counts.
-constexpr int kChunkWarps = 8;
-constexpr int kMaxChunks = 128;
+// More tokens: the router alone, then a CTA per chunk of 1024 pairs counts the
+// chunk's experts, then one places its pairs.  Up to 16 chunks the placing CTAs
+// count all ids themselves, one launch less (T = 1024, k = 8: 4.0 us behind the
+// router against 5.8).  From 32768 counts on, a launch between them adds up the
+// chunks' counts, since every placing CTA would read them all (E = 256, k = 8,
+// launches behind the router: 128 chunks 8.5 us without it, 10.2 with; 256 chunks
+// 18.1 against 11.4; 512 chunks 50 against 18).
+constexpr int kCountChunks = 16;
+constexpr int kSumCounts = 32768;   // counts (chunks x experts, as a power of two) that a placing CTA adds up
 
-template <int PER, int CPL, typename LT>
-__global__ void __launch_bounds__(32 * kChunkWarps, PER <= 8 ? 4 : 2)
-    score_count_kernel(const ScoreArgs a, int32_t* chunk_hist, int* status, int chunk_tokens, int C) {
-    extern __shared__ __align__(16) float scratch[];
-    const int warp = threadIdx.x >> 5;
-    const int sf = scratch_floats<CPL>(a.E, a.n_group > 1);
-    int* hist = reinterpret_cast<int*>(scratch + kChunkWarps * sf);
-    const int chunk = blockIdx.x / C, rank = blockIdx.x - chunk * C;
-    pdl_wait();
-    for (int e = threadIdx.x; e < a.E; e += 32 * kChunkWarps) hist[e] = 0;
-    if (blockIdx.x == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
+__global__ void __launch_bounds__(256) count_kernel(const int32_t* ids, int R, int E, int32_t* chunk_hist,
+                                                    int* status) {
+    __shared__ int hist[kMaxRouteExperts];
+    for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
     __syncthreads();
-    const int t1 = min(a.T, (chunk + 1) * chunk_tokens);
-    for (int t = chunk * chunk_tokens + rank * kChunkWarps + warp; t < t1; t += C * kChunkWarps)
-        score_token<PER, CPL, LT>(a, t, scratch + warp * sf, hist);
-    __syncwarp();
-    cluster_sync_all();
-    pdl_launch();            // not before: the successor's CTAs would take this kernel's places
-    for (int e = rank * 32 * kChunkWarps + threadIdx.x; e < a.E; e += C * 32 * kChunkWarps) {
-        int n = 0;
-        for (int r = 0; r < C; ++r) n += ld_shared_cluster_s32(mapa_shared(smem_u32(hist + e), r));
-        chunk_hist[static_cast<long long>(chunk) * a.E + e] = n;
-    }
-    __syncwarp();
-    cluster_sync_all();      // peers have read this CTA's counts
+    pdl_launch();
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
+    const int p0 = blockIdx.x * kRouteChunk + threadIdx.x;
+    int id[kRouteChunk / 256];
+#pragma unroll
+    for (int i = 0; i < kRouteChunk / 256; ++i) id[i] = p0 + 256 * i < R ? __ldcg(ids + p0 + 256 * i) : -1;
+#pragma unroll
+    for (int i = 0; i < kRouteChunk / 256; ++i)
+        if (id[i] >= 0) atomicAdd(&hist[id[i]], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 256)
+        chunk_hist[static_cast<long long>(blockIdx.x) * E + e] = hist[e];
 }
 
-// Second launch: one CTA per chunk adds up the counts of the chunks before it
-// (every CTA for itself: at most 128 rows of counts out of L2) and places its
-// pairs.  Thread (g, e) of the 1024 reads every G-th row of counts at expert e,
+// Many chunks: the counts of a chunk become the sums up to and with it.  A CTA per
+// 32 experts; its 32 warps take a 32nd of the chunks each, in two passes.
+__global__ void __launch_bounds__(1024) scan_kernel(int32_t* chunk_hist, int E, int nchunks) {
+    __shared__ int sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = 32 * blockIdx.x + lane;
+    const int per = (nchunks + 31) / 32, c0 = min(nchunks, warp * per), c1 = min(nchunks, c0 + per);
+    pdl_launch();
+    pdl_wait();
+    int sum = 0;
+    if (e < E)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += __ldcg(chunk_hist + static_cast<long long>(c) * E + e);
+    sums[warp][lane] = sum;
+    __syncthreads();
+    int run = 0;
+    for (int w = 0; w < warp; ++w) run += sums[w][lane];
+    if (e >= E) return;
+    for (int c = c0; c < c1; c += 8) {
+        int h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            h[i] = c + i < c1 ? __ldcg(chunk_hist + static_cast<long long>(c + i) * E + e) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            run += h[i];
+            if (c + i < c1) chunk_hist[static_cast<long long>(c + i) * E + e] = run;
+        }
+    }
+}
+
+// One CTA per chunk adds up the counts of the chunks before it (every CTA for
+// itself, at most kSumCounts of them out of L2) and places its pairs.  Thread (g, e) of the 1024 reads every G-th row of counts at expert e,
 // so that 64 chunks of 256 experts are one round of 16 loads a thread; 32 warps
-// have one or two steps of 32 pairs each.
+// have one step of 32 pairs each.
 constexpr int kPlaceWarps = 32;
 
-// Without counts from the first launch (COUNT: few chunks, after the router
-// alone), every CTA counts all R ids itself, 8 a thread; the first clears status.
-template <bool COUNT>
+// kCount: without a counting launch before it (few chunks), every CTA counts all R
+// ids itself, 8 a thread; the first clears status.  kPrefix: behind scan_kernel,
+// two rows hold what is needed.
+enum Place { kCount, kSum, kPrefix };
+template <Place MODE>
 __global__ void __launch_bounds__(32 * kPlaceWarps)
-    place_kernel(const int32_t* ids, int R, int E, int nbits, int chunk_pairs, const int32_t* chunk_hist,
-                 int32_t* m_indptr, int32_t* perm, int32_t* inv_perm, int* status) {
+    place_kernel(const int32_t* ids, int R, int E, int nbits, const int32_t* chunk_hist, int32_t* m_indptr,
+                 int32_t* perm, int32_t* inv_perm, int* status) {
     extern __shared__ __align__(16) int smem[];
     __shared__ int warp_tot[kPlaceWarps];
     __shared__ int part_total[32 * kPlaceWarps], part_before[32 * kPlaceWarps];
@@ -716,15 +743,15 @@ __global__ void __launch_bounds__(32 * kPlaceWarps)
     int* base = cnt + kPlaceWarps * E;     // [E]
     const int nchunks = gridDim.x, chunk = blockIdx.x;
     const int e = threadIdx.x & ((1 << nbits) - 1), g = threadIdx.x >> nbits;   // E <= 2^nbits <= 1024
-    const int G = COUNT ? 1 : (32 * kPlaceWarps) >> nbits;
-    const int first = chunk * chunk_pairs;
-    if constexpr (COUNT) {
+    const int G = MODE != kSum ? 1 : (32 * kPlaceWarps) >> nbits;
+    const int first = chunk * kRouteChunk;
+    if constexpr (MODE == kCount) {
         part_total[threadIdx.x] = part_before[threadIdx.x] = 0;
         __syncthreads();
     }
     pdl_wait();
     int total = 0, before = 0;
-    if constexpr (COUNT) {
+    if constexpr (MODE == kCount) {
         if (chunk == 0 && threadIdx.x < kStatusInts) status[threadIdx.x] = 0;
         for (int p0 = threadIdx.x; p0 < R; p0 += 8 * 32 * kPlaceWarps) {
             int id[8];
@@ -740,27 +767,34 @@ __global__ void __launch_bounds__(32 * kPlaceWarps)
                     if (p0 + i * 32 * kPlaceWarps < first) atomicAdd(&part_before[id[i]], 1);
                 }
         }
+    } else if constexpr (MODE == kPrefix) {
+        if (threadIdx.x < E) {
+            total = __ldcg(chunk_hist + static_cast<long long>(nchunks - 1) * E + e);
+            before = chunk ? __ldcg(chunk_hist + static_cast<long long>(chunk - 1) * E + e) : 0;
+        }
+        part_total[threadIdx.x] = total;
+        part_before[threadIdx.x] = before;
     } else {
-    for (int c0 = g; c0 < nchunks; c0 += 16 * G) {
-        int h[16];
+        for (int c0 = g; c0 < nchunks; c0 += 16 * G) {
+            int h[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int c = c0 + i * G;
-            h[i] = c < nchunks && e < E ? __ldcg(chunk_hist + static_cast<long long>(c) * E + e) : 0;
-        }
+            for (int i = 0; i < 16; ++i) {
+                const int c = c0 + i * G;
+                h[i] = c < nchunks && e < E ? __ldcg(chunk_hist + static_cast<long long>(c) * E + e) : 0;
+            }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (c0 + i * G < chunk) before += h[i];
-            total += h[i];
+            for (int i = 0; i < 16; ++i) {
+                if (c0 + i * G < chunk) before += h[i];
+                total += h[i];
+            }
         }
-    }
-    part_total[threadIdx.x] = total;
-    part_before[threadIdx.x] = before;
+        part_total[threadIdx.x] = total;
+        part_before[threadIdx.x] = before;
     }
     for (int i = threadIdx.x; i < kPlaceWarps * E; i += 32 * kPlaceWarps) cnt[i] = 0;
     __syncthreads();
-    Segment<kPlaceWarps, 2> seg;
-    count_pairs(seg, ids, first, min(chunk_pairs, R - first), E, nbits, cnt);
+    Segment<kPlaceWarps, kRouteChunk / 32 / kPlaceWarps> seg;
+    count_pairs(seg, ids, first, min(kRouteChunk, R - first), E, nbits, cnt);
     const bool mine = threadIdx.x < E;     // one thread an expert from here
     total = before = 0;
     if (mine)
@@ -800,22 +834,21 @@ bool smem_ready(Kern kern, size_t bytes, std::atomic<int>& ready_dev) {
     return true;
 }
 
-template <bool COUNT>
-int launch_place(const RouteArgs& r, int chunk_pairs, int nchunks, cudaStream_t s) {
+template <Place MODE>
+int launch_place(const RouteArgs& r, int nchunks, cudaStream_t s) {
     static std::atomic<int> ready{-1};
     const size_t smem = (kPlaceWarps + 1ull) * r.E * sizeof(int);
-    if (!smem_ready(place_kernel<COUNT>, smem, ready)) return ST_CUDA;
-    return launch_dependent(place_kernel<COUNT>, dim3(nchunks), dim3(32 * kPlaceWarps), 0, smem, s, r.topk_ids,
-                            r.T * r.k, r.E, bits_of(r.E), chunk_pairs,
-                            static_cast<const int32_t*>(r.chunk_hist), r.m_indptr, r.perm, r.inv_perm,
-                            r.status) == cudaSuccess ? ST_OK : ST_CUDA;
+    if (!smem_ready(place_kernel<MODE>, smem, ready)) return ST_CUDA;
+    return launch_dependent(place_kernel<MODE>, dim3(nchunks), dim3(32 * kPlaceWarps), 0, smem, s, r.topk_ids,
+                            r.T * r.k, r.E, bits_of(r.E), static_cast<const int32_t*>(r.chunk_hist), r.m_indptr,
+                            r.perm, r.inv_perm, r.status) == cudaSuccess ? ST_OK : ST_CUDA;
 }
 
 template <int PER, int CPL, typename LT>
 int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
     const size_t sf = scratch_floats<CPL>(a.E, a.n_group > 1) * sizeof(float);
     const int R = a.T * a.k;
-    if (r && a.T <= kSmallTokens && R <= kSmallPairs) {
+    if (r && a.T <= kSmallTokens) {
         static std::atomic<int> ready{-1};
         const size_t smem = kSmallWarps * sf + (kSmallWarps + 1ull) * a.E * sizeof(int);
         auto kern = score_route_small<PER, CPL, LT>;
@@ -824,37 +857,23 @@ int launch_inst(const ScoreArgs& a, const RouteArgs* r, cudaStream_t s) {
                                 r->m_indptr, r->perm, r->inv_perm, r->status, bits_of(a.E)) == cudaSuccess
                    ? ST_OK : ST_CUDA;
     }
-    // chunks of whole tokens, at least kRouteChunk pairs each, so that their
-    // counts fit the workspace's
-    const int chunk_tokens = (kRouteChunk + a.k - 1) / a.k;
-    const int nchunks = (a.T + chunk_tokens - 1) / chunk_tokens;
-    const bool count_all = route_single_launch(R);   // at most 8 chunks of pairs
-    if (r && !count_all && nchunks <= kMaxChunks && a.k >= 2) {
-        static std::atomic<int> ready{-1};
-        const size_t smem = kChunkWarps * sf + static_cast<size_t>(a.E) * sizeof(int);
-        const int C = 8;
-        auto kern = score_count_kernel<PER, CPL, LT>;
-        if (!smem_ready(kern, smem, ready)) return ST_CUDA;
-        if (launch_dependent(kern, dim3(nchunks * C), dim3(32 * kChunkWarps), C, smem, s, a, r->chunk_hist,
-                             r->status, chunk_tokens, C) != cudaSuccess)
-            return ST_CUDA;
-        return launch_place<false>(*r, chunk_tokens * a.k, nchunks, s);
-    }
-    if (a.T > 0) {
-        static std::atomic<int> ready{-1};
-        auto kern = score_kernel<PER, CPL, LT>;
-        if (!smem_ready(kern, kScoreWarps * sf, ready)) return ST_CUDA;
-        const unsigned grid = static_cast<unsigned>((a.T + kScoreWarps - 1) / kScoreWarps);
-        if (launch_dependent(kern, dim3(grid), dim3(32 * kScoreWarps), 0, kScoreWarps * sf, s, a) != cudaSuccess)
-            return ST_CUDA;
-    }
-    if (!r) return ST_OK;
-    if (count_all && R > 0) return launch_place<true>(*r, kRouteChunk, (R + kRouteChunk - 1) / kRouteChunk, s);
-    RouteArgs rr = *r;
-    rr.clear_status = 1;
-    if (R > 0 && cudaMemsetAsync(r->status, 0, sizeof(int) * kStatusInts, s) != cudaSuccess)
+    static std::atomic<int> ready{-1};
+    auto kern = score_kernel<PER, CPL, LT>;
+    if (!smem_ready(kern, kScoreWarps * sf, ready)) return ST_CUDA;
+    const unsigned grid = static_cast<unsigned>((a.T + kScoreWarps - 1) / kScoreWarps);
+    if (launch_dependent(kern, dim3(grid), dim3(32 * kScoreWarps), 0, kScoreWarps * sf, s, a) != cudaSuccess)
         return ST_CUDA;
-    return launch_route_permute(rr, s);
+    if (!r) return ST_OK;
+    const int nchunks = (R + kRouteChunk - 1) / kRouteChunk;
+    if (nchunks <= kCountChunks) return launch_place<kCount>(*r, nchunks, s);
+    if (launch_dependent(count_kernel, dim3(nchunks), dim3(256), 0, 0, s, static_cast<const int32_t*>(r->topk_ids),
+                         R, r->E, r->chunk_hist, r->status) != cudaSuccess)
+        return ST_CUDA;
+    if (static_cast<long long>(nchunks) << bits_of(r->E) <= kSumCounts) return launch_place<kSum>(*r, nchunks, s);
+    if (launch_dependent(scan_kernel, dim3((r->E + 31) / 32), dim3(1024), 0, 0, s, r->chunk_hist, r->E, nchunks) !=
+        cudaSuccess)
+        return ST_CUDA;
+    return launch_place<kPrefix>(*r, nchunks, s);
 }
 
 template <int PER, typename LT>

@@ -179,7 +179,7 @@ MOE_API int moe_router_score_topk(const void* logits, int logits_dtype, const fl
  * moe_router_route is for the plain router: topk_ids [T, k], topk_w [T, k],
  * m_indptr [E+1], perm [T*k], inv_perm [T*k] or NULL, ws of at least
  * moe_route_workspace_size(T, k, E) bytes.  A single kernel launch for up to
- * 256 tokens and 4608 pairs, two up to 131072 pairs.  With T = 0 m_indptr is all zero. */
+ * 128 tokens, two up to 16384 pairs, three or four beyond.  With T = 0 m_indptr is all zero. */
 MOE_API int moe_router_score_route(const void* logits, int logits_dtype, const float* bias, int T,
                                    int E, int k, int scoring, int n_group, int topk_group,
                                    int group_top, int renorm, float scale, int32_t* topk_ids,

@@ -86,6 +86,67 @@ def test_block(T, H, I, E, k):
     assert torch.equal(out, first)
 
 
+def _layers(T, H, I, E, k, seed):
+    """Eight chained blocks on one set of buffers, the residual stream updated in
+    place; run(x, each) calls each() after every operator."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    (w13, s13), (w2, s2) = _weights(E, 2 * I, H, g), _weights(E, H, I, g)
+    gamma, bias, gate_w, R = 1 + 0.1 * r(H), 0.1 * r(E), r(E, H) / H ** 0.5, T * k
+    i32 = dict(dtype=torch.int32, device="cuda")
+    h, y, out = (torch.zeros(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    ids, w = torch.empty(T, k, **i32), torch.empty(T, k, device="cuda")
+    m, perm, inv = torch.empty(E + 1, **i32), torch.empty(R, **i32), torch.empty(R, **i32)
+    ws = torch.empty(moe.moe_route_workspace_size(T, k, E), dtype=torch.uint8, device="cuda")
+    xq, xs = torch.empty(R, H, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    hid = torch.empty(R, I, dtype=torch.bfloat16, device="cuda")
+    hq, hs = torch.empty(R, I, dtype=torch.int8, device="cuda"), torch.empty(R, device="cuda")
+    rows, logits = torch.empty(R, H, device="cuda"), torch.empty(T, E, device="cuda")
+    calls = [
+        lambda: moe.moe_rmsnorm_quant(out, gamma, 1e-6, residual=h, residual_out=h, y=y),
+        lambda: torch.matmul(y.float(), gate_w.t(), out=logits),
+        lambda: moe.moe_router_score_route(logits, ids, w, m, perm, inv, ws, bias=bias, scoring="sigmoid",
+                                           n_group=2, topk_group=1, group_top=2),
+        lambda: moe.int8_quantize(y, xq, xs, inv_perm=inv, k=k),
+        lambda: moe.int8_moe_gemm(xq, w13, xs, s13, hid, m_indptr=m, is_gated=True),
+        lambda: moe.int8_quantize(hid, hq, hs),
+        lambda: moe.int8_moe_gemm(hq, w2, hs, s2, rows, m_indptr=m),
+        lambda: moe.moe_combine(rows, inv, w, out)]
+
+    def run(x, each=lambda: None):
+        h.copy_(x)
+        out.copy_(x)
+        for _ in range(8):
+            for call in calls:
+                call()
+                each()
+        return h.clone(), out.clone(), perm.clone()
+    return run
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [(4, 512, 256, 16, 4), (64, 256, 256, 32, 8), (200, 512, 256, 8, 2),
+                                       (3000, 256, 256, 64, 6)])
+def test_chained_blocks_on_two_streams(T, H, I, E, k):
+    """Each operator may start before its predecessor has ended: chained calls
+    without a pause, on two streams at once, give the bits of calls that wait."""
+    a, b = _layers(T, H, I, E, k, 1), _layers(T, H, I, E, k, 2)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    xs = [torch.randn(T, H, generator=g, device="cuda").bfloat16() for _ in range(3)]
+    want = [run(x, torch.cuda.synchronize) for x in xs for run in (a, b)]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        torch.cuda.synchronize()
+        got = []
+        for x in xs:
+            for run, stream in ((a, s1), (b, s2)):
+                with torch.cuda.stream(stream):
+                    got.append(run(x))
+        torch.cuda.synchronize()
+        for u, v in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(u, v))
+    assert moe.moe_get_device_status(None) == moe.MOE_OK
+
+
 def test_norm_rows_feed_the_block_scaled_gemms():
     """The norm's FP8 and MXFP8 rows, in both scale layouts, as the activation
     operand of the existing grouped GEMMs."""

@@ -199,6 +199,35 @@ def test_many_tokens(T, E, k):
     assert torch.equal(m[1:].long(), torch.bincount(flat, minlength=E).cumsum(0)) and int(m[0]) == 0
 
 
+@pytest.mark.parametrize("T,E,k", [
+    (128, 1024, 32), (129, 8, 1), (129, 1024, 32),            # the last call of one launch, the first of two
+    (2048, 40, 8), (2049, 40, 8), (16385, 3, 1),              # 16 and 17 chunks of 1024 pairs
+    (16384, 256, 8), (16400, 256, 8), (32768, 1024, 1),       # 32768 counts of chunks, and more
+    (70000, 8, 2), (262145, 64, 2), (300000, 33, 1), (40001, 500, 10)])
+def test_grouping_at_its_boundaries(T, E, k):
+    """Each way of grouping at its first and last sizes, a status and rows of
+    counts left by an earlier call in the workspace, half of the pairs on one
+    expert."""
+    g = torch.Generator(device="cuda").manual_seed(T + E)
+    logits = torch.randn(T, E, generator=g, device="cuda", dtype=torch.bfloat16)
+    logits[::2, E // 2] = 9.0
+    ids, w, m, perm, inv, ws = buffers(T, E, k)
+    ws.fill_(255)
+    for _ in range(2):
+        perm.fill_(-7)
+        inv.fill_(-7)
+        moe.moe_router_score_route(logits, ids, w, m, perm, inv, ws, renorm=False)
+        assert moe.moe_get_device_status(ws) == moe.MOE_OK
+        flat = ids.flatten().long()
+        assert torch.equal(perm.long(), torch.sort(flat, stable=True).indices)
+        assert torch.equal(inv.long()[perm.long()], torch.arange(T * k, device="cuda"))
+        assert torch.equal(m[1:].long(), torch.bincount(flat, minlength=E).cumsum(0)) and int(m[0]) == 0
+    two, w2 = torch.full_like(ids, -7), torch.full_like(w, -7.0)
+    moe.moe_router_score_topk(logits, two, w2, renorm=False)
+    assert torch.equal(two, ids) and torch.equal(w2, w)
+    assert bool((ids[::2, 0] == E // 2).all())
+
+
 def test_no_tokens():
     ids, w, m, perm, inv, ws = buffers(0, 16, 4)
     logits = torch.empty(0, 16, device="cuda")
