@@ -332,7 +332,8 @@ static int check_score(const void* logits, int logits_dtype, const float* bias, 
         return MOE_ERR_INVALID_ARG;
     if (k > topk_group * (E / n_group)) return MOE_ERR_INVALID_ARG;
     if (!(scale > 0.0f) || scale > 3.402823466e38f) return MOE_ERR_INVALID_ARG;
-    if (static_cast<long long>(T) * k > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+    // pairs and tokens rounded up to whole CTAs are still an int
+    if (static_cast<long long>(T) * k > 0x7ffff000ll) return MOE_ERR_UNSUPPORTED;
     if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
     if (!aligned4(logits) || !aligned4(bias) || !aligned4(ids) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;

@@ -164,7 +164,7 @@ MOE_API int moe_router_route(const float* logits, int T, int E, int k, int32_t* 
  *  renorm    0 or 1;  scale  finite, > 0
  *  topk_ids  device int32 [T, k] out;  topk_w device fp32 [T, k] out
  * Limits and errors as for moe_router_topk (k <= MOE_ROUTER_MAX_K,
- * E <= MOE_MAX_EXPERTS); T = 0 is a no-op. */
+ * E <= MOE_MAX_EXPERTS); T * k up to 2^31 - 4096; T = 0 is a no-op. */
 #define MOE_DTYPE_F32 0
 #define MOE_DTYPE_BF16 1
 #define MOE_SCORE_SOFTMAX 0

@@ -182,7 +182,7 @@ def test_far_logits(scoring):
 
 @pytest.mark.parametrize("T,E,k", [(5000, 40, 1), (9000, 16, 1), (20000, 64, 8), (2049, 512, 32), (16384, 1024, 8)])
 def test_many_tokens(T, E, k):
-    """Each way of grouping (one launch after the router, three, two with counts)."""
+    """Each way of grouping: ids counted by the placing launch, before it, and summed up before it."""
     g = torch.Generator(device="cuda").manual_seed(T)
     logits = torch.randn(T, E, generator=g, device="cuda")
     ids, w, m, perm, inv, ws = buffers(T, E, k)

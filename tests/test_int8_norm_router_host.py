@@ -31,7 +31,8 @@ def _score(T=8, E=64, k=4, logits=FAKE, ids=FAKE, w=FAKE, logits_dtype="float32"
     (dict(group_top=3), INVALID), (dict(n_group=32, topk_group=1, k=3), INVALID),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(logits=0), INVALID), (dict(ids=0), INVALID),
-    (dict(w=0), INVALID), (dict(T=1 << 28, k=32, E=64), UNSUPPORTED), (dict(logits=FAKE + 2), INVALID),
+    (dict(w=0), INVALID), (dict(T=1 << 28, k=32, E=64), UNSUPPORTED), (dict(T=2 ** 31 - 1, k=1), UNSUPPORTED),
+    (dict(logits=FAKE + 2), INVALID),
     (dict(ids=FAKE + 1), INVALID), (dict(w=FAKE + 2), INVALID), (dict(bias=FAKE + 2), INVALID),
 ])
 def test_score_refusals(args, want):
