@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 2 ? 512 : 1024, V == 2 && !W
         float w[8] = {};
         if (live) {
             if (p.weight_bf16) {
-                unpack8(__ldg(static_cast<const uint4*>(p.weight) + c), w);
+                unpack8(static_cast<const uint4*>(p.weight)[c], w);
             } else {
-                const float4 a = __ldg(static_cast<const float4*>(p.weight) + 2 * c);
-                const float4 b = __ldg(static_cast<const float4*>(p.weight) + 2 * c + 1);
+                const float4 a = static_cast<const float4*>(p.weight)[2 * c];
+                const float4 b = static_cast<const float4*>(p.weight)[2 * c + 1];
                 w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
                 w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
             }
@@ -253,9 +253,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 2 ? 512 : 1024, V == 2 && !W
 // WIDE: CTAs of more than 256 threads, or several copies a row.
 template <bool WARP, int V, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
-    int8_quant_kernel(const __nv_bfloat16* __restrict__ xin, int T, int K, int k, int R,
-                      const int32_t* __restrict__ inv_perm, int8_t* __restrict__ q,
-                      float* __restrict__ q_scale) {
+    int8_quant_kernel(const __nv_bfloat16* xin, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
+                      float* q_scale) {
     // 65536 x 2048: one group a thread 92 us, four 68, and 59.5 (1.04 of the copy
     // rate) with six CTAs of 256 threads an SM (40 registers); with eight copies a
     // row the stores bound it, and fewer CTAs keep their runs longer: 8192 x 7168
@@ -274,6 +273,8 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
         const int c = threadIdx.x + i * TPR;
         xr[i] = row_ok && c < nvec ? x[c] : make_uint4(0, 0, 0, 0);
     }
+    const int32_t* to = inv_perm + static_cast<long long>(t) * k;
+    int row = inv_perm && row_ok ? to[0] : t;   // under the row's own loads
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -291,15 +292,18 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
         codes[i] = int8_codes(f, g.inv);
     }
     for (int j = 0; j < k; ++j) {
-        const int row = inv_perm ? inv_perm[static_cast<long long>(t) * k + j] : t;
-        if (row < 0 || row >= R) continue;
-        uint2* dst = reinterpret_cast<uint2*>(q) + static_cast<long long>(row) * nvec;
+        // read ahead of the stores: for all the compiler knows they could change it
+        const int next = j + 1 < k ? to[j + 1] : -1;
+        if (row >= 0 && row < R) {
+            uint2* dst = reinterpret_cast<uint2*>(q) + static_cast<long long>(row) * nvec;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int c = threadIdx.x + i * TPR;
-            if (c < nvec) dst[c] = codes[i];
+            for (int i = 0; i < V; ++i) {
+                const int c = threadIdx.x + i * TPR;
+                if (c < nvec) dst[c] = codes[i];
+            }
+            if (threadIdx.x == 0) q_scale[row] = g.scale;
         }
-        if (threadIdx.x == 0) q_scale[row] = g.scale;
+        row = next;
     }
 }
 

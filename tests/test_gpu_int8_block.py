@@ -177,3 +177,40 @@ def test_norm_rows_feed_the_block_scaled_gemms():
         moe.moe_rmsnorm_quant(x, gamma, 1e-6, q_format="mxfp8", q=q, q_scale=sf, scale_major=major)
         moe.mxfp8_moe_gemm(q, wq, sf, tiled, m, out, a_sf_major=major)
         assert float((out.double() - want).norm() / want.norm()) < 2.0 ** -4
+
+
+def test_inputs_rewritten_by_the_kernel_before():
+    """Each operator may be resident before its predecessor has ended, and reads
+    what that one writes: norm weights, rows and destination rows rewritten by
+    the call before, without a pause, give the bits of calls that wait."""
+    T, H, E, k, n = 64, 1024, 16, 2, 48
+    g = torch.Generator(device="cuda").manual_seed(12)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    gammas, xs, logits = r(6, 1, H).bfloat16(), r(6, T, H).bfloat16(), r(6, T, E)
+    ones, i32 = torch.ones(H, device="cuda"), dict(dtype=torch.int32, device="cuda")
+    weight = torch.zeros(1, H, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    ids, w, m = torch.empty(T, k, **i32), torch.empty(T, k, device="cuda"), torch.empty(E + 1, **i32)
+    perm, inv = torch.zeros(T * k, **i32), torch.zeros(T * k, **i32)
+    ws = torch.empty(moe.moe_route_workspace_size(T, k, E), dtype=torch.uint8, device="cuda")
+
+    def run(each=lambda: None):
+        q = torch.zeros(n, T * k, H, dtype=torch.int8, device="cuda")
+        s, ys = torch.zeros(n, T * k, device="cuda"), torch.zeros(n, T, H, dtype=torch.bfloat16, device="cuda")
+        q1, s1 = torch.zeros(n, T, H, dtype=torch.int8, device="cuda"), torch.zeros(n, T, device="cuda")
+        for i in range(n):
+            j = i % 6
+            for call in (lambda: moe.moe_rmsnorm_quant(gammas[j], ones, 1e-6, y=weight),
+                         lambda: moe.moe_rmsnorm_quant(xs[j], weight[0], 1e-6, y=ys[i]),
+                         lambda: moe.moe_rmsnorm_quant(xs[-j], weight[0], 1e-6, y=y),
+                         lambda: moe.int8_quantize(y, q1[i], s1[i]),
+                         lambda: moe.moe_router_score_route(logits[j], ids, w, m, perm, inv, ws),
+                         lambda: moe.int8_quantize(y, q[i], s[i], inv_perm=inv, k=k)):
+                call()
+                each()
+        torch.cuda.synchronize()
+        return q, s, ys, q1, s1
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(4):
+        assert all(torch.equal(a, b) for a, b in zip(run(), want))

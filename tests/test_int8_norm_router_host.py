@@ -153,3 +153,19 @@ def test_every_entry_point_documented():
     for name in ("moe_router_score_topk", "moe_router_score_route", "moe_rmsnorm_quant", "int8_quantize",
                  "int8_moe_gemm"):
         assert name in readme
+
+
+def test_dependent_kernels_read_coherently():
+    """A kernel that may be resident before its predecessor has ended must not
+    read that one's outputs through the read-only path: neither __ldg nor a
+    pointer declared as never written while the kernel runs."""
+    root = os.path.dirname(os.path.abspath(moe.__file__))
+    seen = 0
+    for name in sorted(os.listdir(os.path.join(root, "csrc"))):
+        text = open(os.path.join(root, "csrc", name)).read()
+        code = "\n".join(line.split("//")[0] for line in text.splitlines())
+        if name.endswith(".cu") and "pdl_wait(" in code:
+            seen += 1
+            for word in ("__ldg(", "__restrict__", "ld.global.nc"):
+                assert word not in code, f"{name}: {word}"
+    assert seen >= 3
