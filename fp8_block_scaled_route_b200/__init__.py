@@ -743,6 +743,8 @@ def int8_moe_gemm(a, b, a_scale, b_scale, out, *, m_indptr=None, is_gated=False,
         tc = _tc or _torch()
         R, K = a.shape
         bs = b.shape
+        if len(bs) != 2 and len(bs) != 3:
+            raise ValueError(f"{where}: b has shape {tuple(bs)}, expected [E, N, K] or [N, K]")
         E, N = (bs[0], bs[1]) if len(bs) == 3 else (1, bs[0])
         dev = a.get_device()
         n_out = N // 2 if is_gated else N

@@ -169,3 +169,13 @@ def test_dependent_kernels_read_coherently():
             for word in ("__ldg(", "__restrict__", "ld.global.nc"):
                 assert word not in code, f"{name}: {word}"
     assert seen >= 3
+
+
+@pytest.mark.parametrize("shape", [(64,), (32, 1, 1, 64), ()])
+def test_gemm_weights_have_two_or_three_dimensions(shape):
+    """Weights of another rank are named as what is wrong: a vector of K codes
+    would be read as K rows of them."""
+    a, b = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(shape, dtype=torch.int8)
+    n = shape[0] if shape else 64
+    with pytest.raises(ValueError, match="b has"):
+        moe.int8_moe_gemm(a, b, torch.ones(4), torch.ones(n), torch.empty(4, n))
