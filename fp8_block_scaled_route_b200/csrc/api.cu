@@ -393,6 +393,10 @@ int moe_rmsnorm_quant(const void* x, const void* residual, const void* weight, i
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
         !aligned16(y) || !aligned16(q) || !aligned4(q_scale))
         return MOE_ERR_INVALID_ARG;
+    // one buffer for two outputs, or 8-bit rows (half as long) over the rows they come from
+    if (T > 0 && y && y == residual_out) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && q_format != MOE_Q_NONE && (q == y || q == residual_out || q == x || q == residual))
+        return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
     const RmsNormArgs p{x, residual, weight, weight_dtype == MOE_DTYPE_BF16, eps, T, H,

@@ -220,7 +220,9 @@ MOE_API int moe_router_score_route(const void* logits, int logits_dtype, const f
  * 0 < eps <= 1.  H a multiple of 16 (128 with MOE_Q_FP8 and MOE_Q_MXFP8), at
  * most MOE_NORM_MAX_H (else MOE_ERR_UNSUPPORTED).  At least one of y and q is
  * written.  T = 0 is a no-op.  Buffers 16-byte aligned (q_scale 4); apart from
- * the aliases named above no output overlaps another buffer. */
+ * the aliases named above no output overlaps another buffer (residual_out and y
+ * in one buffer, or q in that of x, residual, residual_out or y, is
+ * MOE_ERR_INVALID_ARG). */
 #define MOE_Q_NONE 0
 #define MOE_Q_FP8 1
 #define MOE_Q_MXFP8 2

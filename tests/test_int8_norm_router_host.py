@@ -179,3 +179,16 @@ def test_gemm_weights_have_two_or_three_dimensions(shape):
     n = shape[0] if shape else 64
     with pytest.raises(ValueError, match="b has"):
         moe.int8_moe_gemm(a, b, torch.ones(4), torch.ones(n), torch.empty(4, n))
+
+
+@pytest.mark.parametrize("how", [
+    dict(residual=FAKE, residual_out=3 * FAKE, y=3 * FAKE), dict(residual=2 * FAKE, residual_out=FAKE, y=FAKE),
+    dict(y=3 * FAKE, q_format="int8", q=3 * FAKE, q_scale=4 * FAKE),
+    dict(y=3 * FAKE, q_format="int8", q=FAKE, q_scale=4 * FAKE),
+    dict(residual=2 * FAKE, residual_out=3 * FAKE, y=4 * FAKE, q_format="fp8", q=3 * FAKE, q_scale=5 * FAKE),
+    dict(residual=2 * FAKE, y=4 * FAKE, q_format="mxfp8", q=2 * FAKE, q_scale=5 * FAKE),
+])
+def test_norm_refuses_one_buffer_for_two_outputs(how):
+    """Two outputs in one buffer, or 8-bit rows over the rows they come from:
+    each row would overwrite what another still needs."""
+    assert _norm(weight=9 * FAKE, **how) == INVALID
