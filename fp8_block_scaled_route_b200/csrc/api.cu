@@ -73,6 +73,7 @@ const DevInfo* dev_info() {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -335,7 +336,9 @@ static int check_score(const void* logits, int logits_dtype, const float* bias, 
     // pairs and tokens rounded up to whole CTAs are still an int
     if (static_cast<long long>(T) * k > 0x7ffff000ll) return MOE_ERR_UNSUPPORTED;
     if (T > 0 && (!logits || !ids || !w)) return MOE_ERR_INVALID_ARG;
-    if (!aligned4(logits) || !aligned4(bias) || !aligned4(ids) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
+    // bf16 logits may start at any element: the kernels load them one by one
+    const bool logits_ok = logits_dtype == MOE_DTYPE_BF16 ? aligned2(logits) : aligned4(logits);
+    if (!logits_ok || !aligned4(bias) || !aligned4(ids) || !aligned4(w)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -163,6 +163,7 @@ MOE_API int moe_router_route(const float* logits, int T, int E, int k, int32_t* 
  *            1 <= topk_group <= n_group; k <= topk_group * E / n_group
  *  renorm    0 or 1;  scale  finite, > 0
  *  topk_ids  device int32 [T, k] out;  topk_w device fp32 [T, k] out
+ * Every buffer aligned to its element's size.
  * Limits and errors as for moe_router_topk (k <= MOE_ROUTER_MAX_K,
  * E <= MOE_MAX_EXPERTS); T * k up to 2^31 - 4096; T = 0 is a no-op. */
 #define MOE_DTYPE_F32 0

@@ -257,3 +257,12 @@ def test_stream_capture_and_no_inverse():
         r_ids, _ = reference(logits, 4, None, "softmax", 1, 1, 1, True, 1.0)
         assert torch.equal(ids.cpu(), r_ids)
         assert torch.equal(perm.cpu().long(), torch.sort(r_ids.flatten().long(), stable=True).indices)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+def test_bf16_logits_at_any_element(T):
+    """bf16 logits that start on an odd element, as rows cut out of a larger tensor do."""
+    g = torch.Generator().manual_seed(10)
+    rows = torch.randn(T + 1, 33, generator=g).bfloat16().cuda()
+    assert rows[1:].data_ptr() % 4 == 2
+    check(rows[1:], 4, None, "softmax")

@@ -192,3 +192,8 @@ def test_norm_refuses_one_buffer_for_two_outputs(how):
     """Two outputs in one buffer, or 8-bit rows over the rows they come from:
     each row would overwrite what another still needs."""
     assert _norm(weight=9 * FAKE, **how) == INVALID
+
+
+def test_bf16_logits_are_aligned_to_their_size():
+    assert _score(logits=FAKE + 1, logits_dtype="bfloat16") == INVALID
+    assert _score(logits=FAKE + 2, logits_dtype="bfloat16", ids=FAKE + 2) == INVALID
