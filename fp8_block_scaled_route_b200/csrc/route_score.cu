@@ -68,6 +68,9 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 //  no bias (group values, sums of scores): relative, with arguments up to 88
 //    (2 + 1.7 * 88) 2^-23 a side, 2^-14; below 1e-36 scores lose bits to
 //    underflow.
+// Half of it bounds one value's own error.  A group's value t1 + t2 is off by
+// its terms' roundings, so v is |t1| + |t2| there: with biases of 1e4 and -1e4
+// that is 2e4, and the sum about 1.
 __device__ __forceinline__ float score_tol(const ScoreArgs& a, float v) {
     const float m = fabsf(v);
     if (!a.bias) return 6.103515625e-05f * m + 1e-36f;
@@ -190,9 +193,10 @@ __device__ __forceinline__ int group_lanes_log2(int n_group) {
 }
 
 // Group values and ranks from the E selection values in scratch (-inf where
-// masked): lane's group is lane >> lp; gv its value, returns its rank.
+// masked): lane's group is lane >> lp; gv its value, size the sum of its terms'
+// magnitudes, returns its rank.
 template <typename T>
-__device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch, T& gv) {
+__device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch, T& gv, T& size) {
     const int lane = threadIdx.x & 31;
     const int lp = group_lanes_log2(a.n_group), gs = a.E / a.n_group;
     const int grp = lane >> lp;
@@ -210,7 +214,9 @@ __device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch,
         t2 = max(min(t1, u1), max(t2, u2));
         t1 = max(t1, u1);
     }
-    gv = a.group_top == 2 && t2 > ninf ? t1 + t2 : t1;
+    const bool two = a.group_top == 2 && t2 > ninf;
+    gv = two ? t1 + t2 : t1;
+    size = two ? abs(t1) + abs(t2) : abs(t1);
     int rank = 0;
     for (int o = 0; o < a.n_group; ++o) {
         const T ov = __shfl_sync(0xffffffffu, gv, o << lp);
@@ -236,8 +242,8 @@ __device__ __noinline__ uint32_t choose_groups_f64(const ScoreArgs& a, const LT*
         scratch[e] = s;
     }
     __syncwarp();
-    double gv;
-    const int rank = rank_groups(a, scratch, gv);
+    double gv, size;
+    const int rank = rank_groups(a, scratch, gv, size);
     const int grp = lane >> group_lanes_log2(a.n_group);
     return __ballot_sync(0xffffffffu, grp < a.n_group && rank < a.topk_group);
 }
@@ -334,19 +340,20 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
         __syncwarp();
         // the lanes of a group (2^lp of them, 2^lp * n_group <= 32) scan it together
         const int lp = group_lanes_log2(a.n_group), grp = lane >> lp;
-        float gv;
-        const int rank = rank_groups(a, scratch, gv);
+        float gv, size;
+        const int rank = rank_groups(a, scratch, gv, size);
         const bool in = grp < a.n_group && rank < a.topk_group;
         uint32_t lanes_in = __ballot_sync(0xffffffffu, in);
         if (need_score && a.topk_group < a.n_group) {
+            // every chosen group's least possible value above every other's largest?
             const bool live = grp < a.n_group && gv > ninf;
-            const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(gv) : 0xffffffffu);
-            const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(gv) : 0u);
-            if (lo != 0xffffffffu && hi != 0u) {
-                const float fl = key_value(lo), fh = key_value(hi);
-                if (!(fl - fh > fmaxf(score_tol(a, fl), score_tol(a, fh))))
-                    lanes_in = choose_groups_f64(a, l, reinterpret_cast<double*>(scratch));
-            }
+            const bool finite = size <= kFltMax;
+            const float err = 0.5f * score_tol(a, size);
+            const float least = finite ? gv - err : ninf, most = finite ? gv + err : -ninf;
+            const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(least) : 0xffffffffu);
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(most) : 0u);
+            if (lo != 0xffffffffu && hi != 0u && !(key_value(lo) > key_value(hi)))
+                lanes_in = choose_groups_f64(a, l, reinterpret_cast<double*>(scratch));
         }
         // e / gs = e * inv_gs >> 20 for e, gs <= 1024
         const uint32_t inv_gs = ((1u << 20) + gs - 1) / gs;

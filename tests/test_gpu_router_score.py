@@ -266,3 +266,23 @@ def test_bf16_logits_at_any_element(T):
     rows = torch.randn(T + 1, 33, generator=g).bfloat16().cuda()
     assert rows[1:].data_ptr() % 4 == 2
     check(rows[1:], 4, None, "softmax")
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_group_sums_that_cancel(scoring):
+    """A group's two largest values nearly cancel: their fp32 sum is rounded at
+    the size of its terms, far above its own, and the chosen groups are still
+    those of the 64-bit sums."""
+    if scoring == "sigmoid":
+        check(torch.tensor([[0.0012, 0.0012, 0.0020, 0.0]]).cuda(), 2,
+              torch.tensor([1e4, -1e4, 1e4, -1e4]).cuda(), scoring, 2, 1, 2)
+    g = torch.Generator().manual_seed(8)
+    for big in (100.0, 1e4, 1e6):
+        logits = torch.randn(600, 32, generator=g) * (1e-7 * big)
+        bias = torch.tensor([big, -big]).repeat(16)
+        check(logits.cuda(), 4, bias.cuda(), scoring, 16, 5, 2, span=1.0)
+        # some groups cancel, some have two experts in reach, some one of them
+        bias[8:16] = 0.1 * torch.randn(8, generator=g)
+        bias[17:21:2] = -1e9
+        check(logits.cuda(), 4, bias.cuda(), scoring, 16, 5, 2, span=1.0)
+        check(logits.cuda(), 8, bias.cuda(), scoring, 8, 3, 2, span=1.0)
