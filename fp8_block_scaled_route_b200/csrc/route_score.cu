@@ -194,7 +194,7 @@ __device__ __forceinline__ int group_lanes_log2(int n_group) {
 
 // Group values and ranks from the E selection values in scratch (-inf where
 // masked): lane's group is lane >> lp; gv its value, size the sum of its terms'
-// magnitudes, returns its rank.
+// magnitudes (-1 where every expert is masked), returns its rank.
 template <typename T>
 __device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch, T& gv, T& size) {
     const int lane = threadIdx.x & 31;
@@ -216,7 +216,7 @@ __device__ __forceinline__ int rank_groups(const ScoreArgs& a, const T* scratch,
     }
     const bool two = a.group_top == 2 && t2 > ninf;
     gv = two ? t1 + t2 : t1;
-    size = two ? abs(t1) + abs(t2) : abs(t1);
+    size = !(t1 > ninf) ? static_cast<T>(-1) : two ? abs(t1) + abs(t2) : abs(t1);
     int rank = 0;
     for (int o = 0; o < a.n_group; ++o) {
         const T ov = __shfl_sync(0xffffffffu, gv, o << lp);
@@ -346,13 +346,15 @@ __device__ __forceinline__ void score_token(const ScoreArgs& a, int t, float* sc
         uint32_t lanes_in = __ballot_sync(0xffffffffu, in);
         if (need_score && a.topk_group < a.n_group) {
             // every chosen group's least possible value above every other's largest?
-            const bool live = grp < a.n_group && gv > ninf;
+            // (two biases near -FLT_MAX add up to -infinity: such a group is none of
+            // masked experts, and only its 64-bit value tells its place)
+            const bool live = grp < a.n_group && size >= 0.0f;
             const bool finite = size <= kFltMax;
             const float err = 0.5f * score_tol(a, size);
             const float least = finite ? gv - err : ninf, most = finite ? gv + err : -ninf;
             const uint32_t lo = __reduce_min_sync(0xffffffffu, in && live ? order_key(least) : 0xffffffffu);
             const uint32_t hi = __reduce_max_sync(0xffffffffu, !in && live ? order_key(most) : 0u);
-            if (lo != 0xffffffffu && hi != 0u && !(key_value(lo) > key_value(hi)))
+            if (hi != 0u && (lo == 0xffffffffu || !(key_value(lo) > key_value(hi))))
                 lanes_in = choose_groups_f64(a, l, reinterpret_cast<double*>(scratch));
         }
         // e / gs = e * inv_gs >> 20 for e, gs <= 1024

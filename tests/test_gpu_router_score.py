@@ -286,3 +286,17 @@ def test_group_sums_that_cancel(scoring):
         bias[17:21:2] = -1e9
         check(logits.cuda(), 4, bias.cuda(), scoring, 16, 5, 2, span=1.0)
         check(logits.cuda(), 8, bias.cuda(), scoring, 8, 3, 2, span=1.0)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_group_sums_beyond_fp32(scoring):
+    """Biases near fp32's ends: a group whose sum leaves fp32's range is not one
+    of masked experts, and keeps its place among its like."""
+    g = torch.Generator().manual_seed(9)
+    logits = torch.randn(20, 15, generator=g).cuda()
+    low, b16 = -3.402823466e38, float(torch.finfo(torch.bfloat16).min)
+    for groups in ([low, -3e38, -2.9e38, -3.2e38, -3.1e38], [-3e38, low, low, b16, -2e38],
+                   [low, b16, b16, low, b16], [3e38, 3.1e38, low, 3.2e38, -3e38], [low, -3e38, 0.5, -2e38, 3e38]):
+        bias = torch.tensor(groups).repeat_interleave(3).cuda()
+        for tg in (1, 2, 3, 4):
+            check(logits, 3, bias, scoring, 5, tg, 2)
