@@ -146,6 +146,12 @@ __device__ __forceinline__ int ld_shared_cluster_s32(uint32_t addr) {
 }
 
 // ----------------------------------------------------------------- values
+// Hardware 2^x, within 2^-22 of it, subnormal results kept.
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 // Larger of two values; NaN when either is.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
     float r;

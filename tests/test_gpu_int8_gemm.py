@@ -192,3 +192,30 @@ def test_wait_bound_is_reported_once():
     assert moe.moe_get_device_status(None) == moe.MOE_ERR_DEVICE_TIMEOUT
     assert moe.moe_get_device_status(None) == moe.MOE_OK
     check(300, 512, 4096, 1, counts=[300], seed=3, dense=True)
+
+
+@pytest.mark.parametrize("R,n", [(3, 64), (40, 33), (200, 64), (520, 96)])
+def test_gated_fp32_output_over_the_range(R, n):
+    """fp32 output of the gated product for gates from -100 to 100: SiLU within
+    a few roundings of its value, however far the gate."""
+    K = 16
+    a = torch.zeros(R, K, dtype=torch.int8, device="cuda")
+    a[:, 3] = 1
+    b = torch.zeros(1, 2 * n, K, dtype=torch.int8, device="cuda")
+    g = torch.Generator().manual_seed(R)
+    b[0, :, 3] = torch.randint(1, 128, (2 * n,), generator=g).to(torch.int8)
+    b[0, :n, 3] *= (1 - 2 * (torch.arange(n) % 2)).to(torch.int8).cuda()
+    sa = (torch.rand(R, generator=g) * 0.8).cuda()
+    sb = torch.ones(1, 2 * n, device="cuda")
+    out = torch.empty(R, n, device="cuda")
+    moe.int8_moe_gemm(a, b, sa, sb, out, is_gated=True)
+    G = b[0, :, 3].float() * sa[:, None]               # the fp32 values, sums of one product
+    gate, up = G[:, :n].double(), G[:, n:].double()
+    want = gate * torch.sigmoid(gate) * up
+    assert float(gate.min()) < -60 and float(gate.max()) > 60
+    # z e / (1 + e) with e = exp(-|z|): the exponential by 4 U, its correction by 1 and
+    # by ln 2's rounding (0.05 |z|), the sum by 1, the reciprocal by 2, two products
+    # and that with `up`; below 2^-126 the exponential loses bits (2^-148)
+    tol = (11 + 0.05 * gate.abs()) * U * want.abs() + 2.0 ** -147 * 100 * up.abs()
+    d = (out.double() - want).abs()
+    assert bool((d <= tol).all()), float((d / want.abs().clamp(min=1e-30)).max() / U)
