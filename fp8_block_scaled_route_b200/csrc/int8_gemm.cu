@@ -794,9 +794,21 @@ bool encode(CUtensorMap* m, const void* ptr, int rank, const cuuint64_t* dims, c
             const cuuint32_t* box) {
     auto fn = encode_fn();
     const cuuint32_t es[5] = {1u, 1u, 1u, 1u, 1u};
-    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), dims, strides, box, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto once = [&] {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(ptr), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (!fn) return false;
+    CUresult r = once();
+    if (r == CUDA_ERROR_INVALID_CONTEXT) {
+        // a thread's first use of CUDA: the driver has no context for it yet, and no
+        // runtime call came before this one to give it the current device's
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+        r = once();
+    }
+    return r == CUDA_SUCCESS;
 }
 
 // Map of a row-major int8 matrix [rows, cols] with boxes of box_rows x 128

@@ -214,3 +214,41 @@ def test_inputs_rewritten_by_the_kernel_before():
     want = run(torch.cuda.synchronize)
     for _ in range(4):
         assert all(torch.equal(a, b) for a, b in zip(run(), want))
+
+
+def test_first_call_of_a_thread():
+    """Each operator as a new thread's first use of the GPU: a thread that no call
+    of the CUDA runtime has bound to a context yet."""
+    import threading
+    T, H, E, k = 8, 256, 4, 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, gamma, logits = r(T, H).bfloat16(), torch.ones(H, device="cuda"), r(T, E)
+    y, out = torch.empty_like(x), torch.empty(T, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w, m = torch.empty(T, k, **i32), torch.empty(T, k, device="cuda"), torch.empty(E + 1, **i32)
+    perm, ws = torch.empty(T * k, **i32), torch.empty(moe.moe_route_workspace_size(T, k, E), dtype=torch.uint8,
+                                                      device="cuda")
+    q, s = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    (b, sb), stream = _weights(1, 64, H, g), torch.cuda.Stream()
+    moe.int8_quantize(x, q, s)
+    torch.cuda.synchronize()
+    calls = [lambda h: moe.moe_rmsnorm_quant(x, gamma, 1e-6, y=y, stream=h),
+             lambda h: moe.moe_router_score_topk(logits, ids, w, stream=h),
+             lambda h: moe.moe_router_score_route(logits, ids, w, m, perm, None, ws, stream=h),
+             lambda h: moe.int8_quantize(x, q, s, stream=h),
+             lambda h: moe.int8_moe_gemm(q, b, s, sb, out, stream=h)]
+    for i, call in enumerate(calls):
+        got = []
+
+        def run(call=call):
+            try:
+                got.append(call(stream.cuda_stream))
+            except Exception as e:  # noqa: BLE001  (told to the test's own thread)
+                got.append(e)
+
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert got == [moe.MOE_OK], (i, got)
