@@ -24,7 +24,7 @@ namespace {
 // Status word for the entry points that take no workspace.
 __device__ int g_lib_status[kStatusInts];
 // Status word of int8_moe_gemm: only ever set by its kernels, and cleared when
-// it is read, so that a call costs no clearing launch.
+// it is read (I8Errors), so that a call costs no clearing launch.
 __device__ int g_i8_status[kStatusInts];
 
 std::atomic<unsigned long long> g_timeout_ns{2000000000ull};
@@ -70,6 +70,52 @@ const DevInfo* dev_info() {
         d.ok = true;
     }
     return &d;
+}
+
+// Errors of int8_moe_gemm, one word per device for all streams and threads.  A
+// reader moves an error from the device's word into this count, and every host
+// thread remembers how far it has read, so that no thread takes an error away from
+// another.  A thread's reading starts at its first int8_moe_gemm on the device.
+struct I8Errors {
+    std::mutex mu;
+    std::atomic<unsigned long long> count{0};
+    int code = MOE_OK;            // of the last one
+};
+I8Errors g_i8_errors[kMaxDevices];
+struct I8Seen {
+    unsigned long long count = 0;
+    bool started = false;
+};
+thread_local I8Seen t_i8_seen[kMaxDevices];
+
+inline void i8_start_reading(const DevInfo* d) {
+    I8Seen& seen = t_i8_seen[d - g_dev];
+    if (seen.started) return;
+    seen.started = true;
+    seen.count = g_i8_errors[d - g_dev].count.load();
+}
+
+// The code of an error this thread has not been told of, MOE_OK or MOE_ERR_CUDA.
+// `stream` has been synchronised.
+int i8_read_status(const DevInfo* d, cudaStream_t stream) {
+    I8Errors& err = g_i8_errors[d - g_dev];
+    I8Seen& seen = t_i8_seen[d - g_dev];
+    std::lock_guard<std::mutex> lk(err.mu);
+    int h[kStatusInts] = {0, 0, 0, 0};
+    if (cudaMemcpy(h, d->i8_status, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
+    if (h[0] != MOE_OK) {
+        // counted before it is cleared: an error set in between is one of this count,
+        // which its own thread has not been told either
+        err.code = h[0];
+        ++err.count;
+        if (cudaMemsetAsync(d->i8_status, 0, sizeof(h), stream) != cudaSuccess ||
+            cudaStreamSynchronize(stream) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    seen.started = true;
+    if (seen.count == err.count.load()) return MOE_OK;
+    seen.count = err.count.load();
+    return err.code;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -435,6 +481,7 @@ int int8_moe_gemm(const int8_t* a, const int8_t* b, const float* a_scale, const 
         return MOE_ERR_INVALID_ARG;
     const DevInfo* d = dev_info();
     if (int st = check_device(d)) return st;
+    i8_start_reading(d);
     const I8GemmArgs g{a, b, a_scale, b_scale, m_indptr, out, out_dtype == MOE_DTYPE_BF16, R, N, K, E,
                        is_gated ? 1 : 0, d->i8_status, g_timeout_ns.load(), d->sms};
     return launch_int8_gemm(g, reinterpret_cast<cudaStream_t>(stream));
@@ -1219,15 +1266,12 @@ int moe_get_device_status(const void* ws, moe_stream_t stream) {
     if (!d) return MOE_ERR_CUDA;
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return MOE_ERR_CUDA;
+    // the int8 product's first: it is told once, the other word keeps its error
+    if (!ws)
+        if (int st = i8_read_status(d, reinterpret_cast<cudaStream_t>(stream))) return st;
     int h[kStatusInts] = {0, 0, 0, 0};
     const void* src = ws ? ws : d->lib_status;
     if (cudaMemcpy(h, src, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return MOE_ERR_CUDA;
-    if (!ws && h[0] == MOE_OK) {
-        if (cudaMemcpy(h, d->i8_status, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess)
-            return MOE_ERR_CUDA;
-        if (h[0] != MOE_OK && cudaMemset(d->i8_status, 0, sizeof(h)) != cudaSuccess)
-            return MOE_ERR_CUDA;
-    }
     return h[0];
 }
 

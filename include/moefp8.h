@@ -567,8 +567,8 @@ MOE_API int int8_quantize(const void* x, int T, int K, int k, int R, const int32
  * 16, at most MOE_INT8_MAX_K (the 32-bit sums cannot overflow); any N (gated:
  * even); a, b, out 16-byte aligned.  R = 0 is a no-op.  Device timeouts are
  * read with moe_get_device_status(NULL, stream); unlike the other entry
- * points' errors, one of this call stays until it is read, and reading it
- * clears it. */
+ * points' errors, one of this call stays until it is read, by each host thread
+ * for itself. */
 #define MOE_INT8_MAX_K 131056
 MOE_API int int8_moe_gemm(const int8_t* a, const int8_t* b, const float* a_scale,
                           const float* b_scale, const int32_t* m_indptr, void* out, int out_dtype,
@@ -672,10 +672,15 @@ MOE_API int moe_combine(const float* y, const int32_t* row_of_pair, const float*
 
 /* Synchronises `stream`, then returns the device status word written by the
  * last calls that used `ws` (a moe_fp8_fused / moe_route_permute workspace),
- * or, with ws = NULL, the library's own word used by fp8_groupwise_moe_gemm
- * and swiglu_mxfp8_quant, and if that is clear, the word of int8_moe_gemm.
- * Each entry point clears its word when it starts, except int8_moe_gemm, whose
- * word stays until this call has read it.
+ * or, with ws = NULL, an error of int8_moe_gemm that this host thread has not
+ * been told of yet, and if there is none, the library's own word used by
+ * fp8_groupwise_moe_gemm and swiglu_mxfp8_quant.  Each entry point clears its
+ * word when it starts, except int8_moe_gemm: its errors are the device's, of
+ * every stream and thread (`stream` is only what is waited for).  A thread is
+ * told once of all that came since its last read, counted from its first
+ * int8_moe_gemm on (a thread that calls none: from the first one of any), calls
+ * that still run as it reads among them: it may be told of another thread's
+ * call, and another thread's read takes nothing away from it.
  * Returns MOE_OK, MOE_ERR_DEVICE_TIMEOUT, MOE_ERR_BAD_EXPERT_ID or
  * MOE_ERR_CUDA (the synchronise or the read failed). */
 MOE_API int moe_get_device_status(const void* ws, moe_stream_t stream);

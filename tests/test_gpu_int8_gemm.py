@@ -219,3 +219,71 @@ def test_gated_fp32_output_over_the_range(R, n):
     tol = (11 + 0.05 * gate.abs()) * U * want.abs() + 2.0 ** -147 * 100 * up.abs()
     d = (out.double() - want).abs()
     assert bool((d <= tol).all()), float((d / want.abs().clamp(min=1e-30)).max() / U)
+
+
+def _run_out(a, b, sa, sb, out):
+    """A call whose waits run out."""
+    try:
+        moe.moe_set_wait_timeout_ns(1)
+        moe.int8_moe_gemm(a, b, sa, sb, out)
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_timeout_ns(2_000_000_000)
+
+
+def test_status_reaches_every_thread():
+    """A timeout that one thread reads and clears is still told to the thread
+    whose call it was, once."""
+    import threading
+    a, b, sa, sb = make(40, 256, 2048, 1, 4)
+    out = torch.empty(40, 256, dtype=torch.bfloat16, device="cuda")
+    ran, read, got = threading.Event(), threading.Event(), []
+
+    def caller():
+        torch.cuda.set_device(0)
+        _run_out(a, b, sa, sb, out)
+        ran.set()
+        read.wait(60)
+        got.extend(moe.moe_get_device_status(None) for _ in range(2))
+
+    assert moe.moe_get_device_status(None) == moe.MOE_OK
+    t = threading.Thread(target=caller)
+    t.start()
+    assert ran.wait(60)
+    first = [moe.moe_get_device_status(None) for _ in range(2)]
+    read.set()
+    t.join()
+    assert first == [moe.MOE_ERR_DEVICE_TIMEOUT, moe.MOE_OK]
+    assert got == [moe.MOE_ERR_DEVICE_TIMEOUT, moe.MOE_OK]
+
+    def later():     # a thread whose calls come after all that
+        moe.int8_moe_gemm(a, b, sa, sb, out)
+        got.append(moe.moe_get_device_status(None))
+
+    t = threading.Thread(target=later)
+    t.start()
+    t.join()
+    assert got[2:] == [moe.MOE_OK]
+
+
+def test_status_is_not_hidden_by_the_fp8_word():
+    """With both words set each is reported: the int8 one once, the other until
+    its entry point's next call."""
+    import synth
+    inp = synth.make_grouped_gemm_inputs(0, 256, 512, 2, seed=3, group_sizes=[30, 7], device="cuda")
+    fp8_out = torch.zeros(37, 128, dtype=torch.bfloat16, device="cuda")
+    fp8 = lambda: moe.fp8_groupwise_moe_gemm(inp["a"], inp["b"], inp["a_scale"], inp["b_scale"],  # noqa: E731
+                                             inp["m_indptr"], fp8_out, "K", (1, 128, 128), True, -1, -1)
+    a, b, sa, sb = make(40, 256, 2048, 1, 4)
+    out = torch.empty(40, 256, dtype=torch.bfloat16, device="cuda")
+    try:
+        moe.moe_set_wait_timeout_ns(1)
+        fp8()
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_timeout_ns(2_000_000_000)
+    _run_out(a, b, sa, sb, out)
+    assert moe.moe_get_device_status(None) == moe.MOE_ERR_DEVICE_TIMEOUT
+    assert moe.moe_get_device_status(None) == moe.MOE_ERR_DEVICE_TIMEOUT
+    fp8()
+    assert moe.moe_get_device_status(None) == moe.MOE_OK
