@@ -287,3 +287,20 @@ def test_status_is_not_hidden_by_the_fp8_word():
     assert moe.moe_get_device_status(None) == moe.MOE_ERR_DEVICE_TIMEOUT
     fp8()
     assert moe.moe_get_device_status(None) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("R,N,K,E", [(20, 256, 4096, 1), (1000, 384, 640, 20), (4000, 1024, 512, 4)])
+def test_wait_bound_on_the_other_paths(R, N, K, E):
+    """A 1 ns bound on the waits of tiles split over a cluster, of the walk over an
+    item table and of the persistent CTA pairs."""
+    a, b, sa, sb = make(R, N, K, E, 3)
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    m = torch.arange(E + 1, dtype=torch.int32, device="cuda") * (R // E)
+    try:
+        moe.moe_set_wait_timeout_ns(1)
+        moe.int8_moe_gemm(a, b, sa, sb, out, m_indptr=m)
+    finally:
+        moe.moe_set_wait_timeout_ns(2_000_000_000)
+    assert moe.moe_get_device_status(None) == moe.MOE_ERR_DEVICE_TIMEOUT
+    assert moe.moe_get_device_status(None) == moe.MOE_OK
+    check(R, N, K, E, seed=3)
