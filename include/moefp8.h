@@ -149,7 +149,9 @@ MOE_API int moe_router_route(const float* logits, int T, int E, int k, int32_t* 
  *   expert; topk_w_j = p_j, with renorm divided by the sum of the k p_j, times
  *   scale.
  * The choice is the one of 64-bit values of c and of the group values, so it
- * does not depend on 32-bit rounding; the weights are fp32.
+ * does not depend on 32-bit rounding; the weights are fp32, off by at most
+ * (64 + d) 2^-24 of their value with d the distance of the expert's logit from
+ * the largest (with renorm the largest chosen) one.
  * An expert is masked when its logit is NaN or at most the lowest finite
  * value of its type (so also -infinity), or its bias NaN or at most -FLT_MAX:
  * it takes no part in softmax and group values, ranks after every other
@@ -208,9 +210,13 @@ MOE_API int moe_router_score_route(const void* logits, int logits_dtype, const f
  *   MOE_Q_INT8   scale = amax/127 per row, fp32 [T], as int8_moe_gemm reads
  *                (scale_major is not used)
  * Codes are y times the fp32 reciprocal 448/amax (127/amax), rounded to
- * nearest even; a group whose amax is below 2^-100 gets scale 1 and codes 0
- * (MXFP8: the rule of swiglu_mxfp8_quant).  A NaN or infinity in a row makes
- * that row's y NaN or 0 and its scales NaN (E8M0: code 255).
+ * nearest even; a group whose amax is below 2^-100 gets scale 1 and codes of
+ * value 0 (MXFP8: the rule of swiglu_mxfp8_quant).  A NaN in a row makes all its
+ * y and scales NaN (E8M0: code 255).  An infinity of h makes its own y NaN and,
+ * by r = 0, the rest of the row 0: the scale of its group (with MOE_Q_INT8 the
+ * row) is NaN, the other groups' that of zeros.  A y beyond fp32's range makes
+ * its group's scale infinite (E8M0: code 255).  Codes under a scale that is not
+ * finite: int8 0, E4M3 any.
  *  x             device bf16 [T, H]
  *  residual      device bf16 [T, H] or NULL
  *  weight        device [H], fp32 or bf16 (weight_dtype)

@@ -265,3 +265,46 @@ def test_side_stream_and_capture():
     graph.replay()
     torch.cuda.synchronize()
     check_rows("int8", False, q, s, reference(x, res, w, 1e-6)[1])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp8", "int8"])
+def test_norm_rows_that_are_not_finite(fmt):
+    """What a NaN, an infinity and a y beyond fp32 leave in every group of their row."""
+    T, H = 5, 512
+    x, _, _ = make(T, H, 11)
+    res = torch.zeros_like(x)
+    w = torch.ones(H, device="cuda")
+    x[0, 300] = math.nan
+    x[1, 300] = -math.inf
+    x[2, 300] = res[2, 300] = 3e38            # an infinity as bf16(x + residual)
+    w[130] = 3.4e38
+    x[3] = 1.0
+    x[3, 130] = 64.0
+    x[4] = 1.0
+    x[4, 130] = 0.0
+    q, s = outputs(T, H, fmt, False)
+    y = torch.empty_like(x)
+    moe.moe_rmsnorm_quant(x, w, 1e-6, residual=res, y=y, q_format=fmt, q=q[:T], q_scale=s)
+    assert bool(torch.isnan(y[0]).all())
+    for t in (1, 2):
+        assert bool(torch.isnan(y[t, 300])) and bool((torch.cat([y[t, :300], y[t, 301:]]) == 0).all())
+    assert bool(torch.isinf(y[3, 130])) and bool(torch.isfinite(y[3, 131:]).all())
+    if fmt == "int8":
+        assert bool(torch.isnan(s[:3]).all()) and bool(torch.isinf(s[3])) and bool((q[:4] == 0).all())
+        return
+    v = q[:T].view(torch.float8_e4m3fn).float()
+    blk = 128 if fmt == "fp8" else 32
+    hit, over = 300 // blk, 130 // blk
+    bad = torch.isnan(s) if fmt == "fp8" else s == 255
+    clean = s == 1 if fmt == "fp8" else s == 0
+    want = torch.zeros_like(bad)
+    want[0], want[1, hit], want[2, hit] = True, True, True
+    if fmt == "mxfp8":
+        want[3, over] = True
+    else:
+        assert bool(torch.isinf(s[3, over]))
+    assert torch.equal(bad, want)
+    for t in (1, 2):
+        others = torch.arange(H // blk, device="cuda") != hit
+        assert bool(clean[t][others].all())
+        assert bool((v[t].view(-1, blk)[others] == 0).all())
