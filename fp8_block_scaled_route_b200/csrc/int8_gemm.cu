@@ -277,7 +277,8 @@ __device__ __forceinline__ Item item_of(const I8Params& p, int bt, const int* st
 
 // ------------------------------------------------------------ narrow kernel
 // Tiles of 128 weight rows x up to BT token rows, two CTAs an SM, each with a
-// ring of NST stages.
+// ring of NST stages (with BT = 16 the item table leaves room for both up to 895
+// experts; beyond, the grid's second half runs after the first).
 //  SPLIT = false: CTAs walk over the item table, the next items' loads running
 //    under an item's epilogue (4096 rows of 128 experts 1536 x 2048 gated: one
 //    CTA per tile 73 us, walking 70.8; and a crowded expert's token blocks are
@@ -866,7 +867,8 @@ int pair_clusters(int ctas) {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     std::atomic<int>& k = known[ctas == 4 ? 0 : 1];
-    if (k.load() >= 0 && k.load() >> 16 == dev) return k.load() & 0xffff;
+    const int have = k.load();   // once: another thread may put another device's in
+    if (have >= 0 && have >> 16 == dev) return have & 0xffff;
     static std::atomic<int> ready_dev{-1};
     auto kern = int8_pair_kernel<false, true, true>;
     if (!smem_ready(kern, Pair::SMEM, ready_dev)) return 0;

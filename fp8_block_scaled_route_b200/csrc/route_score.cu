@@ -732,9 +732,10 @@ __global__ void __launch_bounds__(1024) scan_kernel(int32_t* chunk_hist, int E, 
 }
 
 // One CTA per chunk adds up the counts of the chunks before it (every CTA for
-// itself, at most kSumCounts of them out of L2) and places its pairs.  Thread (g, e) of the 1024 reads every G-th row of counts at expert e,
-// so that 64 chunks of 256 experts are one round of 16 loads a thread; 32 warps
-// have one step of 32 pairs each.
+// itself out of L2, where there are at most kSumCounts in all) and places its
+// pairs.  Thread (g, e) of the 1024 reads every G-th row of counts at expert e, so
+// that 64 chunks of 256 experts are one round of 16 loads a thread; 32 warps have
+// one step of 32 pairs each.
 constexpr int kPlaceWarps = 32;
 
 // kCount: without a counting launch before it (few chunks), every CTA counts all R
