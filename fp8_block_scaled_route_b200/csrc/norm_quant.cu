@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(WARP ? 256 : V == 2 ? 512 : 1024, V == 2 && !W
 
 // Row t of x [T, K] -> int8 codes and scale at rows inv_perm[t*k + j] (row t
 // when inv_perm is null); entries outside [0, R) are skipped.
-// WIDE: CTAs of more than 256 threads, or several copies a row.
+// WIDE: CTAs of more than 256 threads, or several copies of a row that a CTA
+// shares (without it such a row has one).
 template <bool WARP, int V, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
     int8_quant_kernel(const __nv_bfloat16* xin, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
@@ -273,8 +274,8 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
         const int c = threadIdx.x + i * TPR;
         xr[i] = row_ok && c < nvec ? x[c] : make_uint4(0, 0, 0, 0);
     }
-    const int32_t* to = inv_perm + static_cast<long long>(t) * k;
-    int row = inv_perm && row_ok ? to[0] : t;   // under the row's own loads
+    int row = t;
+    if (inv_perm && row_ok) row = inv_perm[static_cast<long long>(t) * k];   // under the row's own loads
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -291,9 +292,10 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
         unpack8(xr[i], f);
         codes[i] = int8_codes(f, g.inv);
     }
-    for (int j = 0; j < k; ++j) {
+    const int copies = WARP || WIDE ? k : 1;
+    for (int j = 0; j < copies; ++j) {
         // read ahead of the stores: for all the compiler knows they could change it
-        const int next = j + 1 < k ? to[j + 1] : -1;
+        const int next = j + 1 < copies ? inv_perm[static_cast<long long>(t) * k + j + 1] : -1;
         if (row >= 0 && row < R) {
             uint2* dst = reinterpret_cast<uint2*>(q) + static_cast<long long>(row) * nvec;
 #pragma unroll
