@@ -256,7 +256,7 @@ template <bool WARP, int V, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 6)
     int8_quant_kernel(const __nv_bfloat16* xin, int T, int K, int k, int R, const int32_t* inv_perm, int8_t* q,
                       float* q_scale) {
-    // 65536 x 2048: one group a thread 92 us, four 68, and 59.5 (1.04 of the copy
+    // 65536 x 2048: one group a thread 92 us, four 68, and 59.0 (1.04 of the copy
     // rate) with six CTAs of 256 threads an SM (40 registers); with eight copies a
     // row the stores bound it, and fewer CTAs keep their runs longer: 8192 x 7168
     // 95 us against 101
