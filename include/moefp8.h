@@ -561,7 +561,7 @@ MOE_API int int8_quantize(const void* x, int T, int K, int k, int R, const int32
  *   gated: out[r, i] = silu(G[r, i]) * G[r, N/2+i], out [R, N/2].
  * The products by the scales are fp32 roundings.  An fp32 gated output is off
  * from the formula on the rounded G by at most (11 + 0.05 |G[r, i]|) 2^-24 of its
- * value; before bf16's rounding silu is off by up to 2 + 1.17 |G[r, i]| fp32 ulps.
+ * value (below -87, where exp(G) is subnormal, by 2^-140 |G[r, N/2+i]| more); before bf16's rounding silu is off by up to 2 + 1.17 |G[r, i]| fp32 ulps.
  *  a         device int8 [R, K] grouped rows (any value, -128 included)
  *  b         device int8 [E, N, K]
  *  a_scale   device fp32 [R];  b_scale device fp32 [E, N]
